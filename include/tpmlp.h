@@ -87,7 +87,8 @@ typedef enum {
 typedef enum {
   TPM_OP_SEQ_CHUNK_GEMM = 0, TPM_OP_MLP_FWD = 1, TPM_OP_MLP_BWD = 2,
   TPM_OP_GATED_MLP_FWD = 3, TPM_OP_GATED_MLP_BWD = 4, TPM_OP_MX_MLP_FWD = 5, TPM_OP_FP8_DELAYED_MLP_FWD = 6,
-  TPM_OP_MLP_BWD_FP8 = 7, TPM_OP_CAST_FP8 = 8, TPM_OP_LINEAR_BWD = 9
+  TPM_OP_MLP_BWD_FP8 = 7, TPM_OP_CAST_FP8 = 8, TPM_OP_LINEAR_BWD = 9,
+  TPM_OP_RMSNORM_BWD = 10
 } tpm_op;
 
 #define TPM_MAX_CHUNKS 256
@@ -289,6 +290,80 @@ int partial_reduce_seqshard(int T, int64_t M, int64_t D, int rank,
                             void* out, int64_t ldo, int out_dtype, void* stream);
 
 /*
+ * tp_rmsnorm_fwd -- the token-slice step between two sharded products: the
+ * sum of the T partials of a row-parallel product, its bias, the residual's
+ * addition and the root-mean-square norm of the next block's input, in one
+ * pass ("Tensor and sequence parallelism" and "Tensor parallelism": under
+ * sequence parallelism norm and residual run on the rank's M/T tokens; the
+ * row-parallel bias is added once, after the sum, "Pitfalls"):
+ *
+ *   v[i, :] = sum_{t=0}^{T-1} P_t[i, :] + bias + residual[i, :]   (fp32, ascending t)
+ *   rstd[i] = 1 / sqrt(mean(v[i, :]^2) + eps)
+ *   h = v  (stored),   y[i, :] = v[i, :] * rstd[i] * gamma
+ *
+ * rows = the slice's tokens (M/T), any count >= 0; D >= 1, any value.
+ * partials: P_t starts at partials + t * partial_stride elements, leading
+ *    dimension ldx >= D, x_dtype BF16 or F32.  For a [T, M, D] stack pass the
+ *    address of row rank * M/T; T = 1 is a plain input.
+ * bias [D] (or NULL) and gamma [D]: gamma_dtype BF16 or F32.
+ * residual [rows, ldr >= D] (or NULL) and h [rows, ldh >= D] (or NULL, not
+ *    stored): h_dtype BF16 or F32.  h may be the residual's buffer with the
+ *    same leading dimension; otherwise outputs do not overlap inputs.
+ * rstd [rows] fp32 or NULL: saved for the backward.
+ * y [rows, ldy >= D]: y_dtype BF16, F32, or FP8_E4M3 in one of two forms:
+ *    - y_scale (device fp32, the dequantisation factor fixed before the
+ *      step): codes e4m3(y * fp32(1 / *y_scale)), nearest-even, saturating;
+ *      y_amax_out (device fp32 or NULL, set by the call) receives max |y| of
+ *      the fp32 values.  This is the X of tp_mlp_fwd_delayed.
+ *    - y_mx_scales (tpm_mx_scales_bytes(rows, D) bytes, D % 128 == 0): MXFP8
+ *      blocks of 32 columns in the layout tp_mlp_fwd_mx and
+ *      seq_chunk_gemm_mx read, exponents and codes as seq_chunk_gemm_mx
+ *      writes them; scales of padding rows are 0.
+ * y is computed from the unrounded v.  The sum of squares is fp32: a row
+ * whose squares exceed its range gives rstd = 0.  A row holding an infinity
+ * or a NaN gives NaN where IEEE arithmetic does; other rows are untouched.
+ * Whole 16-byte chunks (D and every leading dimension and partial_stride a
+ * multiple of 8, 16-byte aligned arrays, D <= 32768) take a kernel that reads
+ * each input once; anything else a two-pass kernel with the same rounding.
+ * No workspace.  Asynchronous on `stream`.
+ */
+int tp_rmsnorm_fwd(int T, int64_t rows, int64_t D,
+                   const void* partials, int64_t partial_stride, int64_t ldx, int x_dtype,
+                   const void* bias, const void* gamma, int gamma_dtype, float eps,
+                   const void* residual, int64_t ldr, void* h, int64_t ldh, int h_dtype, float* rstd,
+                   void* y, int64_t ldy, int y_dtype, uint8_t* y_mx_scales, const float* y_scale, float* y_amax_out,
+                   void* stream);
+
+/*
+ * tp_rmsnorm_bwd -- backward of tp_rmsnorm_fwd.  The gradient of y reaches a
+ * rank's token slice as the T partial dX_t of the column-parallel product
+ * behind the norm (tp_mlp_bwd, tp_linear_bwd):
+ *
+ *   dy = sum_{t=0}^{T-1} dP_t;   x = h * rstd;   g = dy * gamma
+ *   dh[i, :]  = rstd[i] (g - x mean(g x)) + dres[i, :]
+ *   dgamma    = sum_i dy[i, :] * x[i, :],   dbias = sum_i dh[i, :]
+ *
+ * dh is the gradient of every addend of v: of each P_t, and of the residual.
+ * h [rows, ldh] and dres [rows, lddres] (or NULL: the gradient that reaches h
+ * past the norm, along the residual stream) of h_dtype; rstd [rows] as saved;
+ * dy partials of dy_dtype, strides as in the forward; dh [rows, lddh] of
+ * dh_dtype.  dh may be dres's buffer (same type and leading dimension), or
+ * dy's with T = 1 (likewise).  dgamma, dbias: [D] fp32 or NULL: this slice's
+ * sums (the ranks' slices add up).  Column sums are taken in fp32 in an order
+ * that depends on rows and D alone, so results are repeatable bit for bit;
+ * rows == 0 sets them to zero.
+ * workspace >= tpm_workspace_bytes(TPM_OP_RMSNORM_BWD, rows, D, 0, T, 1,
+ * dy_dtype) bytes when dgamma or dbias is given; its contents need no
+ * preparation.  Calls that share one must not overlap in time.
+ */
+int tp_rmsnorm_bwd(int T, int64_t rows, int64_t D,
+                   const void* dy_partials, int64_t partial_stride, int64_t lddy, int dy_dtype,
+                   const void* gamma, int gamma_dtype, const void* h, int64_t ldh, const float* rstd,
+                   const void* dres, int64_t lddres, int h_dtype,
+                   void* dh, int64_t lddh, int dh_dtype, float* dgamma, float* dbias,
+                   void* workspace, size_t workspace_bytes, void* stream);
+
+/*
  * tp_gated_mlp_fwd -- rank `rank` of a T-way tensor-parallel gated MLP
  * ("Tensor and sequence parallelism", "Worked example: Partitioning an MLP
  * pair": the expansion and gate weights column-partitioned, the gated
@@ -466,7 +541,7 @@ int tp_mlp_bwd_fp8(int64_t M, int64_t D, int64_t F, int T, int rank,
 /* Device workspace needed by an operation (bytes).  For TPM_OP_MLP_FWD /
  * TPM_OP_MLP_BWD and the gated forms pass (M, N = D, K = F, T); for
  * TPM_OP_SEQ_CHUNK_GEMM and TPM_OP_LINEAR_BWD the sizes are (M, N, K)
- * and T is ignored. */
+ * and T is ignored; TPM_OP_RMSNORM_BWD takes (M = rows, N = D). */
 size_t tpm_workspace_bytes(int op, int64_t M, int64_t N, int64_t K, int T, int num_chunks, int dtype);
 
 /* Enqueue on `stream` a release store of `value` into the device word

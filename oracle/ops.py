@@ -388,6 +388,53 @@ def linear_bwd(x, w, dy):
     return dict(dW=gemm(x.T, dy), dX=gemm(dy, w.T))
 
 
+# ------------------------------------------------- linear layer, fused epilogue
+def linear_fwd(x, w, bias=None, act=ACT_NONE, residual=None, scale=1.0):
+    """Y = act(Z) + residual with Z = X . W * scale + bias (bias [N] added to
+    every row).  Returns dict(Z, Y)."""
+    z = gemm(x, w) * float(scale)
+    if bias is not None:
+        z = z + np.asarray(bias, dtype=np.float64)
+    y = act_fwd(z, act)
+    if residual is not None:
+        y = y + np.asarray(residual, dtype=np.float64)
+    return dict(Z=z, Y=y)
+
+
+def linear_act_bwd(x, w, dy, z=None, act=ACT_NONE):
+    """Backward of linear_fwd: dZ = dY act'(Z), dW = X^T . dZ, dX = dZ . W^T,
+    dbias = sum of dZ over the rows; dY itself is the residual's gradient."""
+    dy = np.asarray(dy, dtype=np.float64)
+    dz = dy if act == ACT_NONE else dy * act_grad(np.asarray(z, dtype=np.float64), act)
+    return dict(dZ=dz, dbias=dz.sum(axis=0), **linear_bwd(x, w, dz))
+
+
+# ------------------------------------------------------- token-slice norm
+def rmsnorm_fwd(partials, gamma, eps, bias=None, residual=None):
+    """The step between two sharded products on a rank's token slice: v = the
+    sum of the partials [T, rows, D], plus bias (once) and residual; y = v
+    over its root mean square, times gamma.  Returns dict(h=v, rstd, y)."""
+    v = np.asarray(partials, dtype=np.float64).sum(axis=0)
+    if bias is not None:
+        v = v + np.asarray(bias, dtype=np.float64)
+    if residual is not None:
+        v = v + np.asarray(residual, dtype=np.float64)
+    rstd = 1.0 / np.sqrt((v * v).sum(axis=1) / v.shape[1] + eps)
+    return dict(h=v, rstd=rstd, y=v * rstd[:, None] * np.asarray(gamma, dtype=np.float64))
+
+
+def rmsnorm_bwd(dy_partials, h, rstd, gamma, dres=None):
+    """Chain rule through y_j = v_j r gamma_j, dr/dv_j = -r^3 v_j / D:
+    dv_j = r (g_j - x_j mean(g x)) with g = dy gamma, x = v r."""
+    dy = np.asarray(dy_partials, dtype=np.float64).sum(axis=0)
+    x = np.asarray(h, dtype=np.float64) * np.asarray(rstd, dtype=np.float64)[:, None]
+    g = dy * np.asarray(gamma, dtype=np.float64)
+    dh = np.asarray(rstd, dtype=np.float64)[:, None] * (g - x * (g * x).mean(axis=1, keepdims=True))
+    if dres is not None:
+        dh = dh + np.asarray(dres, dtype=np.float64)
+    return dict(dh=dh, dgamma=(dy * x).sum(axis=0), dbias=dh.sum(axis=0))
+
+
 # ------------------------------------------------------- gated MLP share
 def gated_mlp_fwd(x, w_gate_t, w_up_t, w_down_t, act=ACT_SILU, store=None):
     """One rank's share of the gated MLP of [WE]:

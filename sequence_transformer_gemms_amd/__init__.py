@@ -14,6 +14,8 @@ Arguments are marshalled to the C ABI; nothing is computed here.
     tp_mlp_fwd_delayed      the fp8 MLP forward under delayed scaling (+ fp8_delayed_scale)
     tp_mlp_bwd_fp8          the MLP backward in fp8 (e5m2 gradients); cast_fp8 the current-scaling cast
     partial_reduce_seqshard sum of T partials over this rank's token slice
+    tp_rmsnorm_fwd          h = sum of T partials + bias + residual; y = RMS norm of h (bf16 / fp32 / e4m3 / MXFP8)
+    tp_rmsnorm_bwd          dh, dgamma, dbias from the T partials of dy
 """
 from __future__ import annotations
 
@@ -25,13 +27,13 @@ from . import _abi
 from ._abi import (ACT_GELU_ERF, ACT_GELU_TANH, ACT_NONE, ACT_RELU, ACT_SILU, BF16, EPI_DACT,  # noqa: F401
                    EPI_DGATED, EPI_FWD, EPI_GATED, F32, FP8_E4M3, FP8_E5M2, OP_CAST_FP8, OP_FP8_DELAYED_MLP_FWD, OP_LINEAR_BWD,
                    OP_GATED_MLP_BWD, OP_GATED_MLP_FWD, OP_MLP_BWD, OP_MLP_BWD_FP8, OP_MLP_FWD, OP_MX_MLP_FWD,
-                   OP_SEQ_CHUNK_GEMM, TpmError, check, lib)
+                   OP_RMSNORM_BWD, OP_SEQ_CHUNK_GEMM, TpmError, check, lib)
 from .streams import masked_streams  # noqa: F401
 
 __all__ = ["seq_chunk_gemm", "seq_chunk_gemm_noalloc", "tp_mlp_fwd", "tp_mlp_bwd", "tp_linear_bwd", "tp_gated_mlp_fwd", "tp_gated_mlp_bwd",
            "seq_chunk_gemm_mx", "tp_mlp_fwd_mx", "mx_scales_bytes", "mx_swizzle_scales",
            "tp_mlp_fwd_delayed", "fp8_delayed_scale", "cast_fp8", "tp_mlp_bwd_fp8",
-           "partial_reduce_seqshard",
+           "partial_reduce_seqshard", "tp_rmsnorm_fwd", "tp_rmsnorm_bwd",
            "workspace_bytes", "alloc_workspace", "signal_chunk", "write_chunks", "poll_device_error",
            "set_wait_limit", "dtype_code", "masked_streams", "TpmError", "lib"]
 
@@ -326,6 +328,139 @@ def partial_reduce_seqshard(partials, out, *, T, rank, M=None, stream=None):
                                      dtype_code(partials.dtype), _ptr(out), _ld(out), dtype_code(out.dtype),
                                      _stream(stream))
     return check(rc)
+
+
+class _on:
+    """The call's device made current for its launches, and the stream they go
+    to: the given one, else torch's current stream on the device that holds
+    the tensors.  Every tensor must be on that one GPU."""
+
+    __slots__ = ("stream", "guard")
+
+    def __init__(self, who, stream, *tensors):
+        dev = None
+        for t in tensors:
+            if t is None:
+                continue
+            if not t.is_cuda:
+                raise ValueError(f"{who}: tensors must be in GPU memory")
+            if dev is None:
+                dev = t.get_device()
+            elif t.get_device() != dev:
+                raise ValueError(f"{who}: tensors on different GPUs")
+        self.guard = None if dev == torch.cuda.current_device() else torch.cuda.device(dev)
+        if stream is None:
+            self.stream = torch.cuda.current_stream(dev).cuda_stream
+        else:
+            self.stream = stream if isinstance(stream, int) else stream.cuda_stream
+
+    def __enter__(self):
+        if self.guard is not None:
+            self.guard.__enter__()
+        return self.stream
+
+    def __exit__(self, *exc):
+        if self.guard is not None:
+            self.guard.__exit__(*exc)
+        return False
+
+
+def _fresh_workspace(nbytes, like, stream):
+    """A workspace for one call on `stream` (None: the current one): torch
+    keeps the memory from other uses until that stream is done with it."""
+    ws = torch.empty(max(nbytes, 1), dtype=torch.uint8, device=like.device)
+    if stream is not None:
+        ws.record_stream(torch.cuda.ExternalStream(stream, device=like.device) if isinstance(stream, int) else stream)
+    return ws
+
+
+def _expect(who, name, t, shape, dtypes=None):
+    """t (or None) has this shape, a unit inner stride and one of the dtypes;
+    its address and row stride (0 for None and for vectors)."""
+    if t is None:
+        return None, 0
+    if t.shape != shape:
+        raise ValueError(f"{who}: {name} has shape {tuple(t.shape)}, not {tuple(shape)}")
+    if dtypes is not None and t.dtype not in dtypes:
+        raise ValueError(f"{who}: {name} has dtype {t.dtype}")
+    n = len(shape)
+    if n and shape[-1] > 1 and t.stride(-1) != 1:
+        raise ValueError(f"{who}: {name} needs a unit inner stride")
+    if n < 2:
+        return t.data_ptr(), 0
+    # (the stride of a single row says nothing: torch leaves it arbitrary)
+    return t.data_ptr(), (t.stride(-2) if shape[-2] > 1 else shape[-1])
+
+
+_FLOATS = (torch.bfloat16, torch.float32)
+_U8 = (torch.uint8,)
+_F32 = (torch.float32,)
+
+
+def _rows_partials(who, name, x):
+    """x [rows, D], or [T, rows, D] partials -> (T, rows, D, address, partial stride, row stride)."""
+    if x.dim() not in (2, 3):
+        raise ValueError(f"{who}: {name} is [rows, D], or [T, rows, D] partials")
+    ptr, ld = _expect(who, name, x, x.shape, _FLOATS)
+    if x.dim() == 2:
+        return 1, x.shape[0], x.shape[1], ptr, 0, ld
+    return x.shape[0], x.shape[1], x.shape[2], ptr, x.stride(0) if x.shape[0] > 1 else 0, ld
+
+
+def tp_rmsnorm_fwd(x, gamma, y, *, bias=None, residual=None, h=None, rstd=None, eps=1e-5, y_scale=None,
+                   amax_out=None, y_scales=None, stream=None):
+    """v = sum_t x[t] + bias + residual; h = v; y = v / sqrt(mean(v^2) + eps) * gamma.
+
+    x [rows, D], or [T, rows, D] partial sums (a rank's slice of a [T, M, D]
+    stack: partials[:, rank * M // T:(rank + 1) * M // T]); gamma, bias [D];
+    residual, h [rows, D] (h may be residual); rstd [rows] fp32; y [rows, D]
+    bf16 / fp32, or uint8 e4m3 codes with y_scale (device fp32, fixed before
+    the step; amax_out gets max|y|) or with y_scales (MXFP8 block scales,
+    mx_scales_bytes(rows, D) uint8)."""
+    who = "tp_rmsnorm_fwd"
+    T, rows, D, xp, stride, ldx = _rows_partials(who, "x", x)
+    gp, _ = _expect(who, "gamma", gamma, (D,), _FLOATS)
+    bp, _ = _expect(who, "bias", bias, (D,), (gamma.dtype,))
+    rp, ldr = _expect(who, "residual", residual, (rows, D), _FLOATS)
+    hp, ldh = _expect(who, "h", h, (rows, D), _FLOATS if residual is None else (residual.dtype,))
+    rsp, _ = _expect(who, "rstd", rstd, (rows,), _F32)
+    yp, ldy = _expect(who, "y", y, (rows, D), (torch.bfloat16, torch.float32, torch.uint8))
+    if y_scales is not None and (y_scales.dtype != torch.uint8 or not y_scales.is_contiguous()
+                                 or y_scales.numel() < mx_scales_bytes(rows, D)):
+        raise ValueError(f"{who}: y_scales is a contiguous uint8 tensor of mx_scales_bytes({rows}, {D}) elements")
+    for name, t in (("y_scale", y_scale), ("amax_out", amax_out)):
+        if t is not None and (t.dtype != torch.float32 or t.numel() != 1):
+            raise ValueError(f"{who}: {name} is one fp32 value")
+    hdt = residual if residual is not None else h if h is not None else x
+    with _on(who, stream, x, gamma, y, bias, residual, h, rstd, y_scale, amax_out, y_scales) as st:
+        return check(lib.tp_rmsnorm_fwd(T, rows, D, xp, stride, ldx, dtype_code(x.dtype),
+                                        bp, gp, dtype_code(gamma.dtype), eps,
+                                        rp, ldr, hp, ldh, dtype_code(hdt.dtype), rsp,
+                                        yp, ldy, dtype_code(y.dtype), _ptr(y_scales), _ptr(y_scale), _ptr(amax_out), st))
+
+
+def tp_rmsnorm_bwd(dy, h, rstd, gamma, dh, *, dres=None, dgamma=None, dbias=None, workspace=None, stream=None):
+    """Backward of tp_rmsnorm_fwd: dy [rows, D], or [T, rows, D] partials; h
+    [rows, D] and rstd [rows] as the forward left them (h is x where the
+    forward had one x, no bias and no residual); dres [rows, D] (h's dtype) the gradient that
+    reaches h past the norm; dh [rows, D] the gradient of every addend of h;
+    dgamma, dbias [D] fp32.  The workspace defaults to a fresh one."""
+    who = "tp_rmsnorm_bwd"
+    T, rows, D, dyp, stride, lddy = _rows_partials(who, "dy", dy)
+    hp, ldh = _expect(who, "h", h, (rows, D), _FLOATS)
+    rsp, _ = _expect(who, "rstd", rstd, (rows,), _F32)
+    gp, _ = _expect(who, "gamma", gamma, (D,), _FLOATS)
+    rp, ldr = _expect(who, "dres", dres, (rows, D), (h.dtype,))
+    dhp, lddh = _expect(who, "dh", dh, (rows, D), _FLOATS)
+    dgp, _ = _expect(who, "dgamma", dgamma, (D,), _F32)
+    dbp, _ = _expect(who, "dbias", dbias, (D,), _F32)
+    with _on(who, stream, dy, h, rstd, gamma, dres, dh, dgamma, dbias, workspace) as st:
+        if workspace is None:
+            workspace = _fresh_workspace(workspace_bytes(OP_RMSNORM_BWD, rows, D, 0, T), dy, stream)
+        return check(lib.tp_rmsnorm_bwd(T, rows, D, dyp, stride, lddy, dtype_code(dy.dtype),
+                                        gp, dtype_code(gamma.dtype), hp, ldh, rsp, rp, ldr, dtype_code(h.dtype),
+                                        dhp, lddh, dtype_code(dh.dtype), dgp, dbp,
+                                        workspace.data_ptr(), workspace.numel(), st))
 
 
 def signal_chunk(flag_tensor, index: int, value: int, stream=None):

@@ -24,7 +24,7 @@ COMMON = [
     "-Xclang", "-target-feature", "-Xclang", "-packed-fp32-ops",
     "-I", os.path.join(ROOT, "include"),
 ]
-SOURCES = ["gemm_mfma.hip", "kernels_misc.hip", "api.cpp"]
+SOURCES = ["gemm_mfma.hip", "kernels_misc.hip", "norm.hip", "api.cpp"]
 HEADERS = ["tpm_device.hpp", "tpm_internal.hpp"]
 
 

@@ -492,6 +492,8 @@ size_t tpm_workspace_bytes(int op, int64_t M, int64_t N, int64_t K, int T, int n
     }
     case TPM_OP_CAST_FP8:
       return kCtrlBytes;
+    case TPM_OP_RMSNORM_BWD:   // (rows, D): the work-groups' column sums of dgamma and dbias
+      return 2 * sizeof(float) * (size_t)norm_bwd_groups(M, N) * (size_t)N;
     case TPM_OP_MLP_BWD_FP8: {
       if (T <= 0) return 0;
       const int64_t D = N, Ft = K / T;
@@ -602,6 +604,111 @@ int seq_chunk_gemm(int64_t M, int64_t N, int64_t K,
     }
   }
   return run_gemm(g, s, who);
+}
+
+}  // extern "C"
+
+// ------------------------------------------------------ token-slice norm
+namespace {
+
+// Whether p may be passed for an array of n elements.
+bool given(const void* p, int64_t n) { return p != nullptr || n == 0; }
+bool float_dt(int dt) { return dt == TPM_F32 || dt == TPM_BF16; }
+
+int check_norm(const char* who, int T, int64_t rows, int64_t D, int64_t stride, int64_t ldx, int x_dtype, int h_dtype,
+               int gamma_dtype) {
+  if (rows < 0 || D < 0) return fail(TPM_EINVAL, "%s: negative size", who);
+  if (T < 1 || T > TPM_MAX_CHUNKS) return fail(TPM_EINVAL, "%s: T must be in [1, %d]", who, TPM_MAX_CHUNKS);
+  if (!float_dt(x_dtype) || !float_dt(h_dtype) || !float_dt(gamma_dtype))
+    return fail(TPM_EINVAL, "%s: input dtypes are BF16 or F32", who);
+  if (rows > 0 && D == 0) return fail(TPM_EINVAL, "%s: rows of no elements have no mean", who);
+  if (rows > INT32_MAX || D > INT32_MAX) return fail(TPM_EUNSUPPORTED, "%s: size >= 2^31", who);
+  if (ldx < D) return fail(TPM_EINVAL, "%s: leading dimension smaller than the row width", who);
+  if (T > 1 && stride < 0) return fail(TPM_EINVAL, "%s: negative partial stride", who);
+  return TPM_OK;
+}
+
+}  // namespace
+
+extern "C" {
+
+int tp_rmsnorm_fwd(int T, int64_t rows, int64_t D,
+                   const void* partials, int64_t partial_stride, int64_t ldx, int x_dtype,
+                   const void* bias, const void* gamma, int gamma_dtype, float eps,
+                   const void* residual, int64_t ldr, void* h, int64_t ldh, int h_dtype, float* rstd,
+                   void* y, int64_t ldy, int y_dtype, uint8_t* y_mx_scales, const float* y_scale, float* y_amax_out,
+                   void* stream) {
+  const char* who = "tp_rmsnorm_fwd";
+  int rc = check_norm(who, T, rows, D, partial_stride, ldx, x_dtype, h_dtype, gamma_dtype);
+  if (rc != TPM_OK) return rc;
+  if (!(eps >= 0.f)) return fail(TPM_EINVAL, "%s: eps must be >= 0", who);
+  const bool fp8 = y_dtype == TPM_FP8_E4M3;
+  if (!fp8 && !float_dt(y_dtype)) return fail(TPM_EINVAL, "%s: y dtype BF16, F32 or FP8_E4M3", who);
+  if (fp8 && (y_mx_scales != nullptr) == (y_scale != nullptr))
+    return fail(TPM_EINVAL, "%s: an fp8 y takes block scales (MXFP8) or a fixed scale, one of them", who);
+  if (!fp8 && (y_mx_scales || y_scale)) return fail(TPM_EINVAL, "%s: output scales given for a non-fp8 y", who);
+  if (y_amax_out && !y_scale) return fail(TPM_EINVAL, "%s: an amax is recorded with a fixed fp8 scale only", who);
+  if (y_mx_scales && D % 128 != 0) return fail(TPM_EUNSUPPORTED, "%s: MXFP8 needs D %% 128 == 0", who);
+  if (y_mx_scales && (double)(rows + 31) * (double)D / 32 >= 4294967040.0)
+    return fail(TPM_EUNSUPPORTED, "%s: block scales span >= 4 GiB", who);
+  if (rows > 0 && (!partials || !gamma || !y)) return fail(TPM_EINVAL, "%s: null pointer", who);
+  if (ldy < D || (residual && ldr < D) || (h && ldh < D))
+    return fail(TPM_EINVAL, "%s: leading dimension smaller than the row width", who);
+  hipStream_t s = (hipStream_t)stream;
+  if (y_amax_out) {
+    hipError_t e = launch_ctrl_init((uint32_t*)y_amax_out, 1, s);
+    if (e != hipSuccess) return hip_fail(e, who);
+  }
+  if (rows == 0) return TPM_OK;
+  NormParams p;
+  std::memset(&p, 0, sizeof(p));
+  p.x = partials; p.x_stride = T > 1 ? partial_stride : 0; p.ldx = ldx; p.T = T;
+  p.bias = bias; p.gamma = gamma; p.eps = eps;
+  p.res = residual; p.ldr = ldr; p.h = h; p.ldh = ldh; p.rstd = rstd;
+  p.y = y; p.ldy = ldy; p.y_mx = y_mx_scales; p.y_scale = y_scale; p.amax = y_amax_out;
+  p.rows = rows; p.D = D;
+  p.x_f32 = x_dtype == TPM_F32; p.h_f32 = h_dtype == TPM_F32; p.g_f32 = gamma_dtype == TPM_F32;
+  p.y_kind = y_mx_scales ? NORM_Y_MX : fp8 ? NORM_Y_E4M3 : y_dtype == TPM_F32 ? NORM_Y_F32 : NORM_Y_BF16;
+  hipError_t e = launch_norm_fwd(p, s);
+  return e == hipSuccess ? TPM_OK : hip_fail(e, who);
+}
+
+int tp_rmsnorm_bwd(int T, int64_t rows, int64_t D,
+                   const void* dy_partials, int64_t partial_stride, int64_t lddy, int dy_dtype,
+                   const void* gamma, int gamma_dtype, const void* h, int64_t ldh, const float* rstd,
+                   const void* dres, int64_t lddres, int h_dtype,
+                   void* dh, int64_t lddh, int dh_dtype, float* dgamma, float* dbias,
+                   void* workspace, size_t workspace_bytes, void* stream) {
+  const char* who = "tp_rmsnorm_bwd";
+  int rc = check_norm(who, T, rows, D, partial_stride, lddy, dy_dtype, h_dtype, gamma_dtype);
+  if (rc != TPM_OK) return rc;
+  if (!float_dt(dh_dtype)) return fail(TPM_EINVAL, "%s: dh dtype BF16 or F32", who);
+  if (rows > 0 && (!dy_partials || !gamma || !h || !rstd || !dh)) return fail(TPM_EINVAL, "%s: null pointer", who);
+  if (ldh < D || lddh < D || (dres && lddres < D))
+    return fail(TPM_EINVAL, "%s: leading dimension smaller than the row width", who);
+  const size_t need = tpm_workspace_bytes(TPM_OP_RMSNORM_BWD, rows, D, 0, T, 1, dy_dtype);
+  if ((dgamma || dbias) && need > 0 && (!workspace || workspace_bytes < need))
+    return fail(TPM_EWORKSPACE, "%s: workspace of %zu bytes required", who, need);
+  hipStream_t s = (hipStream_t)stream;
+  if (rows == 0) {   // the sum over no rows
+    for (float* g : {dgamma, dbias}) {
+      if (!g || D == 0) continue;
+      hipError_t e = launch_ctrl_init((uint32_t*)g, (int)D, s);
+      if (e != hipSuccess) return hip_fail(e, who);
+    }
+    return TPM_OK;
+  }
+  NormParams p;
+  std::memset(&p, 0, sizeof(p));
+  p.x = dy_partials; p.x_stride = T > 1 ? partial_stride : 0; p.ldx = lddy; p.T = T;
+  p.gamma = gamma; p.h = const_cast<void*>(h); p.ldh = ldh; p.rstd = const_cast<float*>(rstd);
+  p.res = dres; p.ldr = lddres; p.y = dh; p.ldy = lddh; p.dgamma = dgamma; p.dbias = dbias;
+  p.part = (float*)workspace;
+  p.rows = rows; p.D = D;
+  p.x_f32 = dy_dtype == TPM_F32; p.h_f32 = h_dtype == TPM_F32; p.g_f32 = gamma_dtype == TPM_F32;
+  p.y_kind = dh_dtype == TPM_F32 ? NORM_Y_F32 : NORM_Y_BF16;
+  hipError_t e = launch_norm_bwd(p, s);
+  return e == hipSuccess ? TPM_OK : hip_fail(e, who);
 }
 
 }  // extern "C"

@@ -89,6 +89,33 @@ struct WriterParams {
   uint8_t copy[kMaxGroups];
 };
 
+// One launch of the token-slice norm, forward or backward (norm.hip).  Row r
+// of an array starts at r * its leading dimension (elements).
+struct NormParams {
+  const void* x;             // forward: partial sums P_t; backward: partials of dy
+  const void* res;           // forward: residual or null; backward: dres or null (type of h)
+  const void* gamma;         // [D]
+  const void* bias;          // forward: [D] or null (type of gamma)
+  void* h;                   // forward: v stored, or null; backward: read
+  void* y;                   // forward: y; backward: dh
+  float* rstd;               // [rows]: forward: written when non-null; backward: read
+  uint8_t* y_mx;             // NORM_Y_MX: block scales (mx_scale_offset)
+  const float* y_scale;      // NORM_Y_E4M3: dequantisation factor of y
+  float* amax;               // NORM_Y_E4M3: atomic max of |y|, or null
+  float* dgamma;             // backward: [D] or null
+  float* dbias;              // backward: [D] or null
+  float* part;               // backward: column sums of each work-group
+  int64_t rows, D, x_stride, ldx, ldr, ldh, ldy;
+  float eps;
+  int T;
+  int x_f32, h_f32, g_f32;   // element types: fp32, else bf16
+  int y_kind;                // NORM_Y_* (backward: type of dh)
+};
+enum { NORM_Y_BF16 = 0, NORM_Y_F32 = 1, NORM_Y_E4M3 = 2, NORM_Y_MX = 3 };
+hipError_t launch_norm_fwd(const NormParams& p, hipStream_t s);
+hipError_t launch_norm_bwd(const NormParams& p, hipStream_t s);
+int norm_bwd_groups(int64_t rows, int64_t D);
+
 // kernels' launchers (return hipError_t of the launch)
 hipError_t launch_gemm_bf16(const GemmParams& p, bool a_kmajor, bool b_kmajor, int grid, hipStream_t s);
 // Two bf16 GEMMs in one persistent launch (p0: both operands MN-major, p1:
