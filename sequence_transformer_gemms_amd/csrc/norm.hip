@@ -16,12 +16,19 @@
 // parallelism", section "Pitfalls": added on every rank it would count T
 // times).  v, the row sums and both column sums are held in fp32; y is
 // computed from the unrounded v, so h and y are each rounded once.
+#include <algorithm>
+#include <type_traits>
+
 #include "tpm_device.hpp"
 #include "tpm_internal.hpp"
 
 namespace tpm {
 
 namespace {
+
+// widest rows held in the registers of 1024 threads: 4 chunks of 8 each, 2 in
+// the backward, which also holds two column sums per column
+constexpr int64_t kNormMaxFwd = 32768, kNormMaxBwd = 16384;
 
 __device__ __forceinline__ float ld_f(const void* p, bool f32, int64_t i) {
   return f32 ? ((const float*)p)[i] : bf16_to_f32(((const uint16_t*)p)[i]);
@@ -155,40 +162,440 @@ __global__ void __launch_bounds__(256) norm_bwd_any(const NormParams p) {
   }
 }
 
-// dgamma and dbias: the work-groups' partial column sums added in work-group
-// order, one column per thread.
-__global__ void __launch_bounds__(256) norm_bwd_columns(const NormParams p, int G) {
-  const int64_t c = (int64_t)blockIdx.x * 256 + threadIdx.x;
-  if (c >= p.D) return;
+// ------------------------------------------------------ a row in registers
+// A thread holds V chunks of eight consecutive columns of its row, chunk u at
+// column 8 (u * NT + t) for thread t of the row's NT, so every load and store
+// of a wave covers contiguous memory and each input is read once.  Loads and
+// stores move 16 bytes at any element address (gfx950 takes unaligned vector
+// accesses), so rows of odd width or stride run here too: where D % 8 != 0
+// the row's last chunk is loaded from column D - 8, `shift` of its elements
+// belong to the chunk before it, are zeroed, and are not stored.
+typedef i32x4 i32x4_any __attribute__((aligned(2)));
+typedef f32x4 f32x4_any __attribute__((aligned(4)));
+typedef i32x2 i32x2_any __attribute__((aligned(1)));
+typedef uint32_t u32_any __attribute__((aligned(1)));
+
+template <bool F32>
+struct Raw8 {   // eight elements as loaded
+  i32x4 a, b;   // (b: fp32 only)
+};
+template <bool F32>
+__device__ __forceinline__ Raw8<F32> load8(const void* p, int64_t i) {
+  Raw8<F32> r;
+  if constexpr (F32) {
+    r.a = __builtin_bit_cast(i32x4, __builtin_nontemporal_load((const f32x4_any*)((const float*)p + i)));
+    r.b = __builtin_bit_cast(i32x4, __builtin_nontemporal_load((const f32x4_any*)((const float*)p + i + 4)));
+  } else {
+    r.a = __builtin_nontemporal_load((const i32x4_any*)((const uint16_t*)p + i));
+  }
+  return r;
+}
+template <bool F32>
+__device__ __forceinline__ void widen8(const Raw8<F32>& r, float (&v)[8]) {
+  if constexpr (F32) {
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      v[e] = __int_as_float(r.a[e]);
+      v[4 + e] = __int_as_float(r.b[e]);
+    }
+  } else {
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      v[2 * e] = __uint_as_float((uint32_t)r.a[e] << 16);
+      v[2 * e + 1] = __uint_as_float((uint32_t)r.a[e] & 0xFFFF0000u);
+    }
+  }
+}
+// gamma or bias: read again for every row, from the caches
+__device__ __forceinline__ void param8(const void* p, bool f32, int64_t i, float (&v)[8]) {
+  if (f32) {
+    const f32x4 a = *(const f32x4_any*)((const float*)p + i), b = *(const f32x4_any*)((const float*)p + i + 4);
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      v[e] = a[e];
+      v[4 + e] = b[e];
+    }
+  } else {
+    Raw8<false> r;
+    r.a = *(const i32x4_any*)((const uint16_t*)p + i);
+    widen8<false>(r, v);
+  }
+}
+template <bool F32>
+__device__ __forceinline__ void store8(void* p, int64_t i, const float (&v)[8], int shift) {
+  if (__builtin_expect(shift != 0, 0)) {
+#pragma unroll
+    for (int e = 1; e < 8; ++e)
+      if (e >= shift) st_f(p, F32, i + e, v[e]);
+    return;
+  }
+  if constexpr (F32) {
+    *(f32x4_any*)((float*)p + i) = f32x4{v[0], v[1], v[2], v[3]};
+    *(f32x4_any*)((float*)p + i + 4) = f32x4{v[4], v[5], v[6], v[7]};
+  } else {
+    i32x4 o;
+#pragma unroll
+    for (int e = 0; e < 4; ++e) o[e] = (int)pack_bf16x2(v[2 * e], v[2 * e + 1]);
+    *(i32x4_any*)((uint16_t*)p + i) = o;
+  }
+}
+__device__ __forceinline__ void codes8(uint8_t* p, const float (&y)[8], int shift) {
+  const uint32_t lo = fp8x4<false>(y[0], y[1], y[2], y[3]), hi = fp8x4<false>(y[4], y[5], y[6], y[7]);
+  if (__builtin_expect(shift != 0, 0)) {
+#pragma unroll
+    for (int e = 1; e < 8; ++e)
+      if (e >= shift) p[e] = (uint8_t)((e < 4 ? lo : hi) >> (8 * (e & 3)));
+    return;
+  }
+  *(i32x2_any*)p = i32x2{(int)lo, (int)hi};
+}
+// sum of the T partials of one chunk, fp32 in ascending t, four loads in flight
+template <bool F32>
+__device__ __forceinline__ void sum_partials(const NormParams& p, int64_t at, float (&v)[8]) {
+  widen8<F32>(load8<F32>(p.x, at), v);
+  int t = 1;
+#pragma unroll 1
+  for (; t + 3 < p.T; t += 4) {
+    Raw8<F32> q[4];
+#pragma unroll
+    for (int k = 0; k < 4; ++k) q[k] = load8<F32>(p.x, at + (int64_t)(t + k) * p.x_stride);
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      float w[8];
+      widen8<F32>(q[k], w);
+#pragma unroll
+      for (int e = 0; e < 8; ++e) v[e] += w[e];
+    }
+  }
+#pragma unroll 1
+  for (; t < p.T; ++t) {
+    float w[8];
+    widen8<F32>(load8<F32>(p.x, at + (int64_t)t * p.x_stride), w);
+#pragma unroll
+    for (int e = 0; e < 8; ++e) v[e] += w[e];
+  }
+}
+
+// Sum over the `waves` (1 .. 16) waves of a row, whose first wave in the
+// work-group is `first`.  Every thread of the work-group calls it.
+__device__ __forceinline__ float row_sum(float v, int first, int waves, float* red) {
+#pragma unroll
+  for (int o = 32; o >= 1; o >>= 1) v += __shfl_xor(v, o, 64);
+  if (waves == 1) return v;
+  if ((threadIdx.x & 63) == 0) red[threadIdx.x >> 6] = v;
+  __syncthreads();
+  float s = 0.f;
+  for (int w = 0; w < waves; ++w) s += red[first + w];
+  return s;
+}
+
+// chunk u of thread t: its first column, or -1 past the row's end; the
+// elements below `shift` are the previous chunk's
+__device__ __forceinline__ int chunk_at(int u, int NT, int t, int D, int& shift) {
+  const int c = 8 * (u * NT + t);
+  shift = 0;
+  if (c + 8 <= D) return c;
+  shift = c + 8 - D;
+  return c < D ? D - 8 : -1;
+}
+__device__ __forceinline__ void drop(float (&v)[8], int shift) {
+  if (shift)
+#pragma unroll
+    for (int e = 0; e < 7; ++e) v[e] = e < shift ? 0.f : v[e];
+}
+
+// FP8: y in one of the two 8-bit forms (a kernel of its own: the encoders'
+// NaN path would cost the other one half its registers).
+template <bool XF, bool HF, int V, bool FP8>
+__global__ void __launch_bounds__(1024, 4) norm_fwd_vec(const NormParams p, int NT) {
+  __shared__ float red[2][16];
+  const int slots = blockDim.x / NT;                  // rows of the work-group
+  const int slot = threadIdx.x / NT;
+  int t = threadIdx.x - slot * NT;
+  const int waves = NT >> 6, wave0 = slot * waves;
+  const int D = (int)p.D;
+  const float q_inv = FP8 && p.y_scale ? 1.0f / *p.y_scale : 1.0f;
+  const float inv_d = 1.0f / (float)D;
+  float lmax = 0.f;
+  int par = 0;
+  // (the loop bound is the work-group's: every thread meets the barriers)
+  for (int64_t row0 = (int64_t)blockIdx.x * slots; row0 < p.rows; row0 += (int64_t)gridDim.x * slots, par ^= 1) {
+    const int64_t row = row0 + slot;
+    const bool live = row < p.rows;
+    asm volatile("" : "+v"(t));   // column offsets are formed per row, not kept for every array
+    float v[V][8];
+    float ss = 0.f;
+#pragma unroll
+    for (int u = 0; u < V; ++u) {
+      int shift;
+      const int c = chunk_at(u, NT, t, D, shift);
+      if (live && c >= 0) {
+        Raw8<HF> rr;
+        if (p.res) rr = load8<HF>(p.res, row * p.ldr + c);
+        sum_partials<XF>(p, row * p.ldx + c, v[u]);
+        if (p.bias) {
+          float w[8];
+          param8(p.bias, p.g_f32, c, w);
+#pragma unroll
+          for (int e = 0; e < 8; ++e) v[u][e] += w[e];
+        }
+        if (p.res) {
+          float w[8];
+          widen8<HF>(rr, w);
+#pragma unroll
+          for (int e = 0; e < 8; ++e) v[u][e] += w[e];
+        }
+        drop(v[u], shift);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) ss = fmaf(v[u][e], v[u][e], ss);
+      }
+    }
+    const float r = 1.0f / sqrtf(row_sum(ss, wave0, waves, red[par]) * inv_d + p.eps);
+    if (!live) continue;
+    if (p.rstd && t == 0) p.rstd[row] = r;
+#pragma unroll
+    for (int u = 0; u < V; ++u) {
+      int shift;
+      const int c = chunk_at(u, NT, t, D, shift);
+      if (c < 0) continue;
+      float y[8];
+      param8(p.gamma, p.g_f32, c, y);
+      if (p.h) store8<HF>(p.h, row * p.ldh + c, v[u], shift);
+#pragma unroll
+      for (int e = 0; e < 8; ++e) y[e] = v[u][e] * r * y[e];
+      if constexpr (!FP8) {
+        if (p.y_kind == NORM_Y_F32) store8<true>(p.y, row * p.ldy + c, y, shift);
+        else store8<false>(p.y, row * p.ldy + c, y, shift);
+      } else if (p.y_kind == NORM_Y_E4M3) {
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+          lmax = fmaxf(lmax, fabsf(y[e]));
+          y[e] *= q_inv;
+        }
+        codes8((uint8_t*)p.y + row * p.ldy + c, y, shift);
+      } else {
+        // a 32-column block is four lanes (D % 128 == 0: all inside the row)
+        float m = 0.f;
+#pragma unroll
+        for (int e = 0; e < 8; ++e) m = fmaxf(m, fabsf(y[e]));
+        m = fmaxf(m, __shfl_xor(m, 1, 64));
+        m = fmaxf(m, __shfl_xor(m, 2, 64));
+        const int E = max((int)((__float_as_uint(m) >> 23) & 0xFFu) - 8, 0);
+        const float inv = __uint_as_float((uint32_t)(254 - E) << 23);   // 2^(127 - E)
+#pragma unroll
+        for (int e = 0; e < 8; ++e) y[e] *= inv;
+        codes8((uint8_t*)p.y + row * p.ldy + c, y, 0);
+        // the four scales of 128 columns are one dword of the row's record
+        uint32_t w = (uint32_t)E << (8 * ((threadIdx.x >> 2) & 3));
+        w |= (uint32_t)__shfl_xor((int)w, 4, 64);
+        w |= (uint32_t)__shfl_xor((int)w, 8, 64);
+        if ((threadIdx.x & 15) == 0)
+          *(u32_any*)(p.y_mx + mx_scale_offset((uint32_t)row, (uint32_t)(c >> 5), (uint32_t)(D >> 7))) = w;
+      }
+    }
+  }
+  if constexpr (FP8) {
+    if (p.y_kind == NORM_Y_MX && blockIdx.x == 0) pad_mx_rows(p);
+    if (p.amax) {
+      __syncthreads();
+      block_amax_to(p.amax, lmax, red[0]);
+    }
+  }
+}
+
+// Backward.  A work-group holds blockDim / NT rows at a time and walks the
+// rows with a stride; each thread keeps the dgamma and dbias sums of its own
+// columns over all the rows it sees.  At the end the row slots' sums are
+// added in LDS and leave as one row of partial sums per work-group.
+template <bool XF, bool HF, int V>
+__global__ void __launch_bounds__(1024) norm_bwd_vec(const NormParams p, int NT) {
+  __shared__ float red[2][16];
+  __shared__ float cols[8192 * V];   // [slot][V * NT * 8]
+  const int slots = blockDim.x / NT;
+  const int slot = threadIdx.x / NT;
+  int t = threadIdx.x - slot * NT;
+  const int waves = NT >> 6, wave0 = slot * waves;
+  const int D = (int)p.D;
+  float sg[V][8], sb[V][8];
+#pragma unroll
+  for (int u = 0; u < V; ++u)
+#pragma unroll
+    for (int e = 0; e < 8; ++e) sg[u][e] = sb[u][e] = 0.f;
+  const float inv_d = 1.0f / (float)D;
+  int par = 0;
+  for (int64_t row0 = (int64_t)blockIdx.x * slots; row0 < p.rows; row0 += (int64_t)gridDim.x * slots, par ^= 1) {
+    const int64_t row = row0 + slot;
+    const bool live = row < p.rows;
+    asm volatile("" : "+v"(t));   // column offsets are formed per row, not kept for every array
+    float dy[V][8];
+    Raw8<HF> hh[V], dres[V];
+    float gx = 0.f;
+    const float r = live ? p.rstd[row] : 0.f;
+#pragma unroll
+    for (int u = 0; u < V; ++u) {
+      int shift;
+      const int c = chunk_at(u, NT, t, D, shift);
+      if (live && c >= 0) {
+        float g[8], x[8];
+        hh[u] = load8<HF>(p.h, row * p.ldh + c);
+        if (p.res) dres[u] = load8<HF>(p.res, row * p.ldr + c);
+        sum_partials<XF>(p, row * p.ldx + c, dy[u]);
+        param8(p.gamma, p.g_f32, c, g);
+        drop(dy[u], shift);
+        widen8<HF>(hh[u], x);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+          x[e] *= r;
+          sg[u][e] = fmaf(dy[u][e], x[e], sg[u][e]);
+          dy[u][e] *= g[e];
+          gx = fmaf(dy[u][e], x[e], gx);
+        }
+      }
+    }
+    const float m = row_sum(gx, wave0, waves, red[par]) * inv_d;
+    if (!live) continue;
+#pragma unroll
+    for (int u = 0; u < V; ++u) {
+      int shift;
+      const int c = chunk_at(u, NT, t, D, shift);
+      if (c < 0) continue;
+      float dh[8], x[8];
+      widen8<HF>(hh[u], x);
+#pragma unroll
+      for (int e = 0; e < 8; ++e) dh[e] = r * (dy[u][e] - x[e] * r * m);
+      if (p.res) {
+        widen8<HF>(dres[u], x);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) dh[e] += x[e];
+      }
+#pragma unroll
+      for (int e = 0; e < 8; ++e) sb[u][e] += dh[e];
+      if (p.y_kind == NORM_Y_F32) store8<true>(p.y, row * p.ldy + c, dh, shift);
+      else store8<false>(p.y, row * p.ldy + c, dh, shift);
+    }
+  }
   for (int which = 0; which < 2; ++which) {
-    float* out = which ? p.dbias : p.dgamma;
-    if (!out) continue;
-    const float* src = p.part + (which ? (int64_t)G * p.D : 0) + c;
-    float s = 0.f;
-    for (int g = 0; g < G; ++g) s += src[(int64_t)g * p.D];
+    if (!(which ? p.dbias : p.dgamma)) continue;
+    float* out = p.part + ((int64_t)which * gridDim.x + blockIdx.x) * p.D;
+    __syncthreads();
+#pragma unroll
+    for (int u = 0; u < V; ++u) {
+      int shift;
+      const int c = chunk_at(u, NT, t, D, shift);
+      if (c < 0) continue;
+      float* to = slots == 1 ? out : cols + slot * (V * NT * 8);
+      store8<true>(to, c, which ? sb[u] : sg[u], shift);
+    }
+    if (slots == 1) continue;
+    __syncthreads();
+    for (int k = threadIdx.x; k < D; k += blockDim.x) {
+      float s = 0.f;
+      for (int i = 0; i < slots; ++i) s += cols[i * (V * NT * 8) + k];
+      out[k] = s;
+    }
+  }
+}
+
+// dgamma and dbias: the work-groups' partial column sums.  A work-group takes
+// 64 columns (a wave's lanes, 256 contiguous bytes of a row of partials); its
+// 16 waves add every 16th partial row each, and the wave sums are added in
+// wave order: a fixed order, and 256 work-groups at D = 8192 with both sums.
+__global__ void __launch_bounds__(1024) norm_bwd_columns(const NormParams p, int G) {
+  __shared__ float red[16][64];
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  const int64_t c = (int64_t)blockIdx.x * 64 + lane;
+  const int which = p.dgamma ? blockIdx.y : 1;
+  float* out = which ? p.dbias : p.dgamma;
+  float s = 0.f;
+  if (c < p.D) {
+    const float* src = p.part + (int64_t)which * G * p.D + c;
+#pragma unroll 8
+    for (int g = wave; g < G; g += 16) s += src[(int64_t)g * p.D];
+  }
+  red[wave][lane] = s;
+  __syncthreads();
+  if (wave == 0 && c < p.D) {
+    for (int w = 1; w < 16; ++w) s += red[w][lane];
     out[c] = s;
   }
 }
 
 }  // namespace
 
-// Work-groups of the backward: each sums its rows' column contributions, so
-// their number fixes the order of the column sums.  It depends on the shape
-// alone, never on the stream.
-int norm_bwd_groups(int64_t rows, int64_t) { return (int)std::min<int64_t>(rows, 256); }
+// Work-groups of the backward.  Each sums its rows' column contributions, so
+// their number fixes the order of the column sums; it depends on the shape
+// alone, never on the stream or the arrays.  1024 threads per CU either way:
+// 512 work-groups of 512 threads where each sees eight rows or more (rows 8192,
+// D 8192: 100 us, 105 with 256 of 1024), 256 of 1024 below, where the partial
+// sums' own traffic counts (T = 8, rows 1024, D 8192: 45 us, 48 with 512).
+int norm_bwd_groups(int64_t rows, int64_t) { return (int)std::min<int64_t>(rows, rows >= 4096 ? 512 : 256); }
+
+// whole waves that cover D columns at V chunks of 8 a thread
+static int row_threads(int64_t D, int V) { return (int)((D + 512 * V - 1) / (512 * V)) * 64; }
+
+template <class F>
+static void with_types(const NormParams& p, F&& f) {
+  using T = std::true_type;
+  using N = std::false_type;
+  if (p.x_f32 && p.h_f32) f(T{}, T{});
+  else if (p.x_f32) f(T{}, N{});
+  else if (p.h_f32) f(N{}, T{});
+  else f(N{}, N{});
+}
+template <class F>
+static void with_chunks(int V, F&& f) {
+  if (V == 1) f(std::integral_constant<int, 1>{});
+  else if (V == 2) f(std::integral_constant<int, 2>{});
+  else f(std::integral_constant<int, 4>{});
+}
 
 hipError_t launch_norm_fwd(const NormParams& p, hipStream_t s) {
-  const int grid = (int)std::min<int64_t>(p.rows, 4096);
-  norm_fwd_any<<<grid, 256, 0, s>>>(p);
+  if (p.D < 8 || p.D > kNormMaxFwd) {
+    norm_fwd_any<<<(int)std::min<int64_t>(p.rows, 4096), 256, 0, s>>>(p);
+    return hipGetLastError();
+  }
+  // Chunks per thread.  Few rows: one, the most threads on each row.  Else
+  // more bytes in flight per row and more rows per CU: rows 1024, D 8192, T = 8
+  // 33 us with four, 37 with two, 43 with one; rows 8192, D 8192, T = 1 88 us
+  // with two, 96 with four, 113 with one; rows 8192, D 16384 194 us with four,
+  // 220 with two.
+  int V = p.rows < 512 ? 1 : (p.T >= 4 || p.D > 8192) ? 4 : 2;
+  while (p.D > 8192 * V) V *= 2;
+  const int NT = row_threads(p.D, V);
+  const int threads = std::max(1, 256 / NT) * NT;
+  const int slots = threads / NT;
+  // a persistent grid of 2048 threads per CU
+  const int grid = (int)std::min<int64_t>((p.rows + slots - 1) / slots, (1 << 19) / threads);
+  with_chunks(V, [&](auto vc) {
+    with_types(p, [&](auto xf, auto hf) {
+      constexpr bool XF = decltype(xf)::value, HF = decltype(hf)::value;
+      constexpr int V = decltype(vc)::value;
+      if (p.y_kind == NORM_Y_E4M3 || p.y_kind == NORM_Y_MX) norm_fwd_vec<XF, HF, V, true><<<grid, threads, 0, s>>>(p, NT);
+      else norm_fwd_vec<XF, HF, V, false><<<grid, threads, 0, s>>>(p, NT);
+    });
+  });
   return hipGetLastError();
 }
 
 hipError_t launch_norm_bwd(const NormParams& p, hipStream_t s) {
   const int G = norm_bwd_groups(p.rows, p.D);
-  norm_bwd_any<<<G, 256, 0, s>>>(p);
+  if (p.D < 8 || p.D > kNormMaxBwd) {
+    norm_bwd_any<<<G, 256, 0, s>>>(p);
+  } else {
+    // two chunks per thread, one where fp32 arrays would spill its registers
+    const int V = (p.x_f32 || p.h_f32) && p.D <= 8192 ? 1 : 2;
+    const int NT = row_threads(p.D, V);
+    const int threads = std::max(1, (p.rows >= 4096 ? 512 : 1024) / NT) * NT;
+    with_types(p, [&](auto xf, auto hf) {
+      constexpr bool XF = decltype(xf)::value, HF = decltype(hf)::value;
+      if (V == 1) norm_bwd_vec<XF, HF, 1><<<G, threads, 0, s>>>(p, NT);
+      else norm_bwd_vec<XF, HF, 2><<<G, threads, 0, s>>>(p, NT);
+    });
+  }
   hipError_t e = hipGetLastError();
   if (e != hipSuccess || (!p.dgamma && !p.dbias)) return e;
-  norm_bwd_columns<<<(unsigned)((p.D + 255) / 256), 256, 0, s>>>(p, G);
+  const dim3 grid((unsigned)((p.D + 63) / 64), p.dgamma && p.dbias ? 2 : 1);
+  norm_bwd_columns<<<grid, 1024, 0, s>>>(p, G);
   return hipGetLastError();
 }
 
