@@ -88,7 +88,7 @@ typedef enum {
   TPM_OP_SEQ_CHUNK_GEMM = 0, TPM_OP_MLP_FWD = 1, TPM_OP_MLP_BWD = 2,
   TPM_OP_GATED_MLP_FWD = 3, TPM_OP_GATED_MLP_BWD = 4, TPM_OP_MX_MLP_FWD = 5, TPM_OP_FP8_DELAYED_MLP_FWD = 6,
   TPM_OP_MLP_BWD_FP8 = 7, TPM_OP_CAST_FP8 = 8, TPM_OP_LINEAR_BWD = 9,
-  TPM_OP_RMSNORM_BWD = 10
+  TPM_OP_RMSNORM_BWD = 10, TPM_OP_LINEAR_FWD = 11, TPM_OP_LINEAR_ACT_BWD = 12
 } tpm_op;
 
 #define TPM_MAX_CHUNKS 256
@@ -270,6 +270,70 @@ int tp_linear_bwd(int64_t M, int64_t N, int64_t K,
                   const void* X, const void* W, const void* dY, int dtype,
                   void* dW, void* dX, int dw_dtype,
                   void* workspace, size_t workspace_bytes, void* stream);
+
+/*
+ * tp_linear_fwd -- one sharded linear layer with its epilogue fused:
+ *
+ *   Z = X . W * x_scale * w_scale + bias     [M, N]
+ *   Y = act(Z) + residual
+ *
+ * X [M, ldx >= K], W [K, ldw >= N], or with trans_w stored [N, ldw >= K];
+ * dtype (of X and W) BF16, F32 or FP8_E4M3; fp32 accumulation.  x_scale,
+ * w_scale: device fp32 dequantisation factors or NULL for 1.
+ * bias [N] (bias_dtype BF16 or F32) or NULL; residual [M, ldr >= N] of
+ * y_dtype or NULL; Z [M, ldz >= N] of y_dtype or NULL receives the
+ * pre-activation, bias included, for tp_linear_act_bwd.  y_dtype BF16 or F32
+ * (F32 with F32 operands).  Y may be the residual's buffer (same leading
+ * dimension); otherwise outputs do not overlap inputs.  On a row-parallel W
+ * bias and residual belong to one rank's call only (they would count T times
+ * in the sum), or to tp_rmsnorm_fwd after the sum.
+ * Chunks of X's rows, chunk_order, chunk_ready and epoch as in
+ * seq_chunk_gemm.
+ * Kernels: the 256 x 256 matrix-core tiles where seq_chunk_gemm's fast-path
+ * conditions hold (bias and residual 16-byte aligned, ldr % 4 == 0); BF16
+ * with M <= 64 (and N, K >= 8) a kernel that streams W once per 16 rows;
+ * other BF16 shapes and alignments, and F32, a 128 x 128 matrix-core kernel
+ * for any shape.  FP8_E4M3 and chunk_ready need the fast-path conditions
+ * (TPM_EUNSUPPORTED otherwise).
+ * workspace (16-byte aligned): required with chunk_ready; with
+ * tpm_workspace_bytes(TPM_OP_LINEAR_FWD, M, N, K, 1, num_chunks, dtype) bytes
+ * the contraction is split over idle CUs, with less or NULL it is not (the
+ * sums then differ in order).  Its contents need no preparation; calls that
+ * share one must not overlap in time.
+ */
+int tp_linear_fwd(int64_t M, int64_t N, int64_t K,
+                  const void* X, int64_t ldx, const float* x_scale,
+                  const void* W, int64_t ldw, int trans_w, const float* w_scale, int dtype,
+                  const void* bias, int bias_dtype, const void* residual, int64_t ldr,
+                  int act, void* Z, int64_t ldz, void* Y, int64_t ldy, int y_dtype,
+                  int num_chunks, const int32_t* chunk_order, const uint32_t* chunk_ready, uint32_t epoch,
+                  void* workspace, size_t workspace_bytes, void* stream);
+
+/*
+ * tp_linear_act_bwd -- backward of tp_linear_fwd (BF16 or F32):
+ *
+ *   dZ = dY * act'(Z)          (stored in dtype for the two products)
+ *   dW = X^T . dZ   [K, N],    dX = dZ . W^T   [M, K],
+ *   dbias[j] = sum_i dZ[i, j]  (fp32, of the unrounded dZ)
+ *
+ * The residual's gradient is dY itself.  X [M, ldx >= K], W [K, ldw >= N],
+ * Z and dY [M, >= N], dX [M, lddx >= K] of dtype; dW [K, lddw >= N] of
+ * dw_dtype (F32 with F32 inputs).  Z is not read with TPM_ACT_NONE (may be
+ * NULL).  dbias [N] fp32 or NULL.  Any sizes: M == 0 writes zeros to dW and
+ * dbias, N == 0 zeros to dX (empty arrays may be NULL).  The two products run
+ * as tp_linear_bwd's paired launch where N and K are multiples of 8 and the
+ * arrays are 16-byte aligned with leading dimensions that are multiples of 8
+ * (outputs of 4), for any M; otherwise, and for F32, on the any-shape
+ * matrix-core kernel.
+ * Results do not depend on timing.  workspace (16-byte aligned) >=
+ * tpm_workspace_bytes(TPM_OP_LINEAR_ACT_BWD, M, N, K, 1, 1, dtype), contents
+ * arbitrary; calls that share one must not overlap in time.
+ */
+int tp_linear_act_bwd(int64_t M, int64_t N, int64_t K,
+                      const void* X, int64_t ldx, const void* W, int64_t ldw,
+                      const void* Z, int64_t ldz, const void* dY, int64_t lddy, int dtype, int act,
+                      void* dW, int64_t lddw, int dw_dtype, void* dX, int64_t lddx, float* dbias,
+                      void* workspace, size_t workspace_bytes, void* stream);
 
 /*
  * partial_reduce_seqshard -- the arithmetic a rank performs in the
@@ -540,8 +604,8 @@ int tp_mlp_bwd_fp8(int64_t M, int64_t D, int64_t F, int T, int rank,
 
 /* Device workspace needed by an operation (bytes).  For TPM_OP_MLP_FWD /
  * TPM_OP_MLP_BWD and the gated forms pass (M, N = D, K = F, T); for
- * TPM_OP_SEQ_CHUNK_GEMM and TPM_OP_LINEAR_BWD the sizes are (M, N, K)
- * and T is ignored; TPM_OP_RMSNORM_BWD takes (M = rows, N = D). */
+ * TPM_OP_SEQ_CHUNK_GEMM, TPM_OP_LINEAR_BWD, TPM_OP_LINEAR_FWD and
+ * TPM_OP_LINEAR_ACT_BWD the sizes are (M, N, K) and T is ignored; TPM_OP_RMSNORM_BWD takes (M = rows, N = D). */
 size_t tpm_workspace_bytes(int op, int64_t M, int64_t N, int64_t K, int T, int num_chunks, int dtype);
 
 /* Enqueue on `stream` a release store of `value` into the device word

@@ -15,6 +15,8 @@ Arguments are marshalled to the C ABI; nothing is computed here.
     tp_mlp_bwd_fp8          the MLP backward in fp8 (e5m2 gradients); cast_fp8 the current-scaling cast
     partial_reduce_seqshard sum of T partials over this rank's token slice
     tp_rmsnorm_fwd          h = sum of T partials + bias + residual; y = RMS norm of h (bf16 / fp32 / e4m3 / MXFP8)
+    tp_linear_fwd           Y = act(X W + bias) + residual, the pre-activation saved
+    tp_linear_act_bwd       its dW, dX and dbias
     tp_rmsnorm_bwd          dh, dgamma, dbias from the T partials of dy
 """
 from __future__ import annotations
@@ -27,13 +29,13 @@ from . import _abi
 from ._abi import (ACT_GELU_ERF, ACT_GELU_TANH, ACT_NONE, ACT_RELU, ACT_SILU, BF16, EPI_DACT,  # noqa: F401
                    EPI_DGATED, EPI_FWD, EPI_GATED, F32, FP8_E4M3, FP8_E5M2, OP_CAST_FP8, OP_FP8_DELAYED_MLP_FWD, OP_LINEAR_BWD,
                    OP_GATED_MLP_BWD, OP_GATED_MLP_FWD, OP_MLP_BWD, OP_MLP_BWD_FP8, OP_MLP_FWD, OP_MX_MLP_FWD,
-                   OP_RMSNORM_BWD, OP_SEQ_CHUNK_GEMM, TpmError, check, lib)
+                   OP_LINEAR_ACT_BWD, OP_LINEAR_FWD, OP_RMSNORM_BWD, OP_SEQ_CHUNK_GEMM, TpmError, check, lib)
 from .streams import masked_streams  # noqa: F401
 
 __all__ = ["seq_chunk_gemm", "seq_chunk_gemm_noalloc", "tp_mlp_fwd", "tp_mlp_bwd", "tp_linear_bwd", "tp_gated_mlp_fwd", "tp_gated_mlp_bwd",
            "seq_chunk_gemm_mx", "tp_mlp_fwd_mx", "mx_scales_bytes", "mx_swizzle_scales",
            "tp_mlp_fwd_delayed", "fp8_delayed_scale", "cast_fp8", "tp_mlp_bwd_fp8",
-           "partial_reduce_seqshard", "tp_rmsnorm_fwd", "tp_rmsnorm_bwd",
+           "partial_reduce_seqshard", "tp_rmsnorm_fwd", "tp_rmsnorm_bwd", "tp_linear_fwd", "tp_linear_act_bwd",
            "workspace_bytes", "alloc_workspace", "signal_chunk", "write_chunks", "poll_device_error",
            "set_wait_limit", "dtype_code", "masked_streams", "TpmError", "lib"]
 
@@ -384,6 +386,8 @@ def _expect(who, name, t, shape, dtypes=None):
     if dtypes is not None and t.dtype not in dtypes:
         raise ValueError(f"{who}: {name} has dtype {t.dtype}")
     n = len(shape)
+    if t.numel() == 0:   # (strides of an empty tensor say nothing)
+        return t.data_ptr(), (shape[-1] if n > 1 else 0)
     if n and shape[-1] > 1 and t.stride(-1) != 1:
         raise ValueError(f"{who}: {name} needs a unit inner stride")
     if n < 2:
@@ -461,6 +465,67 @@ def tp_rmsnorm_bwd(dy, h, rstd, gamma, dh, *, dres=None, dgamma=None, dbias=None
                                         gp, dtype_code(gamma.dtype), hp, ldh, rsp, rp, ldr, dtype_code(h.dtype),
                                         dhp, lddh, dtype_code(dh.dtype), dgp, dbp,
                                         workspace.data_ptr(), workspace.numel(), st))
+
+
+def tp_linear_fwd(X, W, Y, *, bias=None, residual=None, act=ACT_NONE, Z=None, trans_w=False, x_scale=None, w_scale=None,
+                  num_chunks=1, chunk_order=None, chunk_ready=None, epoch=0, workspace=None, stream=None):
+    """Y = act(X W + bias) + residual, Z (optional) = X W + bias.
+
+    X [M, K], W [K, N] (trans_w: stored [N, K]) bf16, fp32, or uint8 e4m3
+    codes with x_scale and w_scale (device fp32; W stored [N, K]); bias [N];
+    residual, Z [M, N] of Y's dtype (Y may be residual); Y bf16 or fp32.  The
+    workspace defaults to a fresh one (pass one that is kept: tpm.alloc_workspace(
+    OP_LINEAR_FWD, M, N, K, 1, num_chunks, dtype_code(X.dtype)))."""
+    who = "tp_linear_fwd"
+    if X.dim() != 2 or W.dim() != 2:
+        raise ValueError(f"{who}: X and W are matrices")
+    M, K = X.shape
+    N = W.shape[0] if trans_w else W.shape[1]
+    dtypes = _FLOATS + _U8 + (torch.float8_e4m3fn,)
+    xp, ldx = _expect(who, "X", X, (M, K), dtypes)
+    wp, ldw = _expect(who, "W", W, (N, K) if trans_w else (K, N), (X.dtype,))
+    yp, ldy = _expect(who, "Y", Y, (M, N), _FLOATS)
+    bp, _ = _expect(who, "bias", bias, (N,), _FLOATS)
+    rp, ldr = _expect(who, "residual", residual, (M, N), (Y.dtype,))
+    zp, ldz = _expect(who, "Z", Z, (M, N), (Y.dtype,))
+    for name, t in (("x_scale", x_scale), ("w_scale", w_scale)):
+        if t is not None and (t.dtype != torch.float32 or t.numel() != 1):
+            raise ValueError(f"{who}: {name} is one fp32 value")
+    code = dtype_code(X.dtype)
+    with _on(who, stream, X, W, Y, bias, residual, Z, x_scale, w_scale, chunk_ready, workspace) as st:
+        if workspace is None:
+            workspace = _fresh_workspace(workspace_bytes(OP_LINEAR_FWD, M, N, K, 1, num_chunks, code), X, stream)
+        return check(lib.tp_linear_fwd(M, N, K, xp, ldx, _ptr(x_scale), wp, ldw, int(trans_w), _ptr(w_scale), code,
+                                       bp, F32 if bias is None else dtype_code(bias.dtype), rp, ldr, act, zp, ldz, yp, ldy,
+                                       dtype_code(Y.dtype), num_chunks, _abi.int_array(chunk_order), _ptr(chunk_ready), epoch,
+                                       workspace.data_ptr(), workspace.numel(), st))
+
+
+def tp_linear_act_bwd(X, W, dY, dW, dX, *, Z=None, act=ACT_NONE, dbias=None, workspace=None, stream=None):
+    """Backward of tp_linear_fwd: dZ = dY act'(Z); dW = X^T dZ, dX = dZ W^T,
+    dbias = sum of dZ over the rows (fp32 [N]).  X [M, K], W [K, N], Z and dY
+    [M, N] bf16 or fp32, dX like X, dW like X or fp32; the residual's gradient
+    is dY.  The workspace defaults to a fresh one (OP_LINEAR_ACT_BWD, M, N, K)."""
+    who = "tp_linear_act_bwd"
+    if X.dim() != 2 or W.dim() != 2:
+        raise ValueError(f"{who}: X and W are matrices")
+    M, K = X.shape
+    N = W.shape[1]
+    same = (X.dtype,)
+    xp, ldx = _expect(who, "X", X, (M, K), _FLOATS)
+    wp, ldw = _expect(who, "W", W, (K, N), same)
+    yp, lddy = _expect(who, "dY", dY, (M, N), same)
+    zp, ldz = _expect(who, "Z", Z, (M, N), same)
+    dwp, lddw = _expect(who, "dW", dW, (K, N), _FLOATS)
+    dxp, lddx = _expect(who, "dX", dX, (M, K), same)
+    dbp, _ = _expect(who, "dbias", dbias, (N,), _F32)
+    code = dtype_code(X.dtype)
+    with _on(who, stream, X, W, dY, Z, dW, dX, dbias, workspace) as st:
+        if workspace is None:
+            workspace = _fresh_workspace(workspace_bytes(OP_LINEAR_ACT_BWD, M, N, K, 1, 1, code), X, stream)
+        return check(lib.tp_linear_act_bwd(M, N, K, xp, ldx, wp, ldw, zp, ldz, yp, lddy, code, act,
+                                           dwp, lddw, dtype_code(dW.dtype), dxp, lddx, dbp,
+                                           workspace.data_ptr(), workspace.numel(), st))
 
 
 def signal_chunk(flag_tensor, index: int, value: int, stream=None):

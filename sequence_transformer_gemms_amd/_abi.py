@@ -27,7 +27,7 @@ EPI_FWD, EPI_DACT, EPI_GATED, EPI_DGATED = 0, 1, 2, 3
 OK, EINVAL, EUNSUPPORTED, EHIP, ETIMEOUT, EWORKSPACE = 0, -1, -2, -3, -4, -5
 (OP_SEQ_CHUNK_GEMM, OP_MLP_FWD, OP_MLP_BWD, OP_GATED_MLP_FWD, OP_GATED_MLP_BWD, OP_MX_MLP_FWD,
  OP_FP8_DELAYED_MLP_FWD, OP_MLP_BWD_FP8, OP_CAST_FP8, OP_LINEAR_BWD,
- OP_RMSNORM_BWD) = 0, 1, 2, 3, 4, 5, 6, 7, 8, 9, 10
+ OP_RMSNORM_BWD, OP_LINEAR_FWD, OP_LINEAR_ACT_BWD) = 0, 1, 2, 3, 4, 5, 6, 7, 8, 9, 10, 11, 12
 MAX_CHUNKS = 256
 
 _i64, _i32, _u32, _vp, _sz = ctypes.c_int64, ctypes.c_int, ctypes.c_uint32, ctypes.c_void_p, ctypes.c_size_t
@@ -68,6 +68,20 @@ lib.tp_linear_bwd.argtypes = [_i64, _i64, _i64,
                               _vp, _vp, _vp, _i32,
                               _vp, _vp, _i32,
                               _vp, _sz, _vp]
+lib.tp_linear_fwd.restype = _i32
+lib.tp_linear_fwd.argtypes = [_i64, _i64, _i64,
+                              _vp, _i64, _vp,
+                              _vp, _i64, _i32, _vp, _i32,
+                              _vp, _i32, _vp, _i64,
+                              _i32, _vp, _i64, _vp, _i64, _i32,
+                              _i32, _vp, _vp, _u32,
+                              _vp, _sz, _vp]
+lib.tp_linear_act_bwd.restype = _i32
+lib.tp_linear_act_bwd.argtypes = [_i64, _i64, _i64,
+                                  _vp, _i64, _vp, _i64,
+                                  _vp, _i64, _vp, _i64, _i32, _i32,
+                                  _vp, _i64, _i32, _vp, _i64, _vp,
+                                  _vp, _sz, _vp]
 lib.tp_rmsnorm_fwd.restype = _i32
 lib.tp_rmsnorm_fwd.argtypes = [_i32, _i64, _i64,
                                _vp, _i64, _i64, _i32,
@@ -154,7 +168,7 @@ lib.tpm_last_error.argtypes = []
 lib.tpm_version.restype = ctypes.c_char_p
 lib.tpm_version.argtypes = []
 
-EXPORTS = ["seq_chunk_gemm", "seq_chunk_gemm_noalloc", "tp_mlp_fwd", "tp_mlp_bwd", "tp_linear_bwd", "tp_rmsnorm_fwd", "tp_rmsnorm_bwd", "tp_gated_mlp_fwd", "tp_gated_mlp_bwd",
+EXPORTS = ["seq_chunk_gemm", "seq_chunk_gemm_noalloc", "tp_mlp_fwd", "tp_mlp_bwd", "tp_linear_bwd", "tp_linear_fwd", "tp_linear_act_bwd", "tp_rmsnorm_fwd", "tp_rmsnorm_bwd", "tp_gated_mlp_fwd", "tp_gated_mlp_bwd",
            "seq_chunk_gemm_mx", "tp_mlp_fwd_mx", "tpm_mx_scales_bytes", "tpm_mx_swizzle_scales",
            "tp_mlp_fwd_delayed", "tpm_fp8_delayed_scale", "tpm_cast_fp8", "tp_mlp_bwd_fp8",
            "partial_reduce_seqshard",

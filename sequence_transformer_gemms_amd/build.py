@@ -24,8 +24,8 @@ COMMON = [
     "-Xclang", "-target-feature", "-Xclang", "-packed-fp32-ops",
     "-I", os.path.join(ROOT, "include"),
 ]
-SOURCES = ["gemm_mfma.hip", "kernels_misc.hip", "norm.hip", "api.cpp"]
-HEADERS = ["tpm_device.hpp", "tpm_internal.hpp"]
+SOURCES = ["gemm_mfma.hip", "gemm_linear.hip", "linear_small.hip", "kernels_misc.hip", "norm.hip", "api.cpp"]
+HEADERS = ["gemm_tile.hpp", "row_vec.hpp", "tpm_device.hpp", "tpm_internal.hpp"]
 
 
 def _compile(src: str, obj: str) -> None:

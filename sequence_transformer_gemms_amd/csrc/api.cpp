@@ -188,6 +188,36 @@ void plan_linear_bwd(int64_t M, int64_t N, int64_t K, int dt, int (&S)[2]) {
   }
 }
 
+// ---- the linear layer's kernels beside the 256 x 256 tiles (linear_small.hip)
+struct RangePlan {
+  int S = 1, per = 1;        // K ranges, steps per range
+};
+RangePlan ranges(int64_t steps, int64_t S) {
+  RangePlan r;
+  steps = std::max<int64_t>(steps, 1);
+  S = std::max<int64_t>(1, std::min(S, steps));
+  r.per = (int)((steps + S - 1) / S);
+  r.S = (int)((steps + r.per - 1) / r.per);
+  return r;
+}
+// Few rows: about four work-groups per CU, so that the whole weight is in flight.
+constexpr int64_t kRowsMax = 64;
+RangePlan plan_rows(int64_t M, int64_t N, int64_t K) {
+  const int64_t tiles = ((N + kRowsTile - 1) / kRowsTile) * ((M + kRowsBlock - 1) / kRowsBlock);
+  return ranges((K + kRowsStep - 1) / kRowsStep, (1023 + tiles) / std::max<int64_t>(tiles, 1));
+}
+// Any shape: K is cut where the 128 x 128 tiles leave CUs idle, two steps a range at least.
+RangePlan plan_any(int64_t M, int64_t N, int64_t K, int dt) {
+  const int64_t tiles = ((M + kAnyTile - 1) / kAnyTile) * ((N + kAnyTile - 1) / kAnyTile);
+  const int64_t steps = (K * esize(dt) + kStepBytes - 1) / kStepBytes;
+  if (tiles >= kPlanCUs || tiles == 0) return ranges(steps, 1);
+  return ranges(steps, std::min<int64_t>({(2 * kPlanCUs + tiles - 1) / tiles, std::max<int64_t>(1, steps / 2), 16}));
+}
+// workspace parts of the linear layer's backward: dZ, and dbias per band of rows
+size_t linear_dz_bytes(int64_t M, int64_t N, int dt) { return round_up((size_t)M * (size_t)N * (size_t)esize(dt), 256); }
+size_t linear_band_bytes(int64_t M, int64_t N) { return round_up((size_t)dact_bands(M, N) * (size_t)N * 4, 256); }
+size_t range_bytes(const RangePlan& r, int64_t M, int64_t N) { return partial_bytes(M, N, r.S); }
+
 struct GemmDesc {
   int64_t M, N, K;
   const void* A; int64_t lda; bool ta; int adt; const float* asc;
@@ -492,6 +522,19 @@ size_t tpm_workspace_bytes(int op, int64_t M, int64_t N, int64_t K, int T, int n
     }
     case TPM_OP_CAST_FP8:
       return kCtrlBytes;
+    case TPM_OP_LINEAR_FWD: {
+      size_t part = plan_bytes(M, N, K, num_chunks, dtype);
+      if (dtype == TPM_BF16 && M <= kRowsMax) part = std::max(part, range_bytes(plan_rows(M, N, K), M, N));
+      if (!is_fp8(dtype)) part = std::max(part, range_bytes(plan_any(M, N, K, dtype), M, N));
+      return kCtrlBytes + part;
+    }
+    case TPM_OP_LINEAR_ACT_BWD: {
+      int S[2];
+      plan_linear_bwd(M, N, K, dtype, S);
+      const size_t pair = partial_bytes(K, N, S[0]) + partial_bytes(M, K, S[1]);
+      const size_t any = std::max(range_bytes(plan_any(K, N, M, dtype), K, N), range_bytes(plan_any(M, K, N, dtype), M, K));
+      return kCtrlBytes + linear_dz_bytes(M, N, dtype) + linear_band_bytes(M, N) + std::max(pair, any);
+    }
     case TPM_OP_RMSNORM_BWD:   // (rows, D): the work-groups' column sums of dgamma and dbias
       return 2 * sizeof(float) * (size_t)norm_bwd_groups(M, N) * (size_t)N;
     case TPM_OP_MLP_BWD_FP8: {
@@ -709,6 +752,172 @@ int tp_rmsnorm_bwd(int T, int64_t rows, int64_t D,
   p.y_kind = dh_dtype == TPM_F32 ? NORM_Y_F32 : NORM_Y_BF16;
   hipError_t e = launch_norm_bwd(p, s);
   return e == hipSuccess ? TPM_OK : hip_fail(e, who);
+}
+
+}  // extern "C"
+
+// ------------------------------------------- linear layer, fused epilogue
+namespace {
+
+// The persistent tile kernel's grid for p on stream s (see run_gemm).
+int tile_grid(const GemmParams& p, hipStream_t s) {
+  const int cus = num_cus(), avail = stream_cus(s);
+  const int grid = std::max(8, (p.ready && avail == cus) ? cus - 8 : avail);
+  return std::min(grid, p.units);
+}
+
+// One product on the any-shape kernel, K cut where the scratch allows it.
+int run_any(const GemmDesc& g, GemmParams& p, hipStream_t s, const char* who) {
+  RangePlan r = plan_any(g.M, g.N, g.K, g.adt);
+  if (r.S > 1 && (!g.part || g.part_bytes < range_bytes(r, g.M, g.N)))
+    r = ranges((g.K * esize(g.adt) + kStepBytes - 1) / kStepBytes, 1);
+  p.splits = r.S;
+  p.ksteps_per_split = r.per;
+  p.partial = g.part;
+  hipError_t e = launch_linear_any(p, g.ta, g.tb, s);
+  return e == hipSuccess ? TPM_OK : hip_fail(e, who);
+}
+
+}  // namespace
+
+extern "C" {
+
+int tp_linear_fwd(int64_t M, int64_t N, int64_t K,
+                  const void* X, int64_t ldx, const float* x_scale,
+                  const void* W, int64_t ldw, int trans_w, const float* w_scale, int dtype,
+                  const void* bias, int bias_dtype, const void* residual, int64_t ldr,
+                  int act, void* Z, int64_t ldz, void* Y, int64_t ldy, int y_dtype,
+                  int num_chunks, const int32_t* chunk_order, const uint32_t* chunk_ready, uint32_t epoch,
+                  void* workspace, size_t workspace_bytes, void* stream) {
+  const char* who = "tp_linear_fwd";
+  if (dtype != TPM_F32 && dtype != TPM_BF16 && dtype != TPM_FP8_E4M3)
+    return fail(TPM_EINVAL, "%s: dtype F32, BF16 or FP8_E4M3", who);
+  if (bias && !float_dt(bias_dtype)) return fail(TPM_EINVAL, "%s: bias dtype BF16 or F32", who);
+  if (!float_dt(y_dtype)) return fail(TPM_EINVAL, "%s: y dtype BF16 or F32", who);
+  if (residual && ldr < N) return fail(TPM_EINVAL, "%s: leading dimension smaller than the row width", who);
+  if (aligned16(workspace) == false) return fail(TPM_EINVAL, "%s: workspace not 16-byte aligned", who);
+  uint32_t* ctrl = ctrl_of(workspace, workspace_bytes);
+  if (chunk_ready && workspace && !ctrl)
+    return fail(TPM_EWORKSPACE, "%s: workspace smaller than %zu bytes", who, kCtrlBytes);
+  GemmDesc g{M, N, K, X, ldx, false, dtype, x_scale, W, ldw, trans_w != 0, dtype, w_scale,
+             Y, ldy, y_dtype, TPM_EPI_FWD, act, Z, ldz, nullptr,
+             num_chunks, chunk_order, chunk_ready, nullptr, epoch, ctrl};
+  if (ctrl) {
+    g.part = (float*)((char*)workspace + kCtrlBytes);
+    g.part_bytes = workspace_bytes - kCtrlBytes;
+  }
+  int rc = check_gemm(g, who);
+  if (rc != TPM_OK) return rc;
+  const char* why = fast_path_blocker(g);
+  if (!why && bias && !aligned16(bias)) why = "bias not 16-byte aligned";
+  if (!why && residual && (!aligned16(residual) || ldr % 4 != 0)) why = "residual not 16-byte aligned or ldr % 4 != 0";
+  if (why && chunk_ready) return fail(TPM_EUNSUPPORTED, "%s: chunk gating needs the matrix-core kernel (%s)", who, why);
+  if (why && is_fp8(dtype)) return fail(TPM_EUNSUPPORTED, "%s: fp8 operands need whole 16-byte chunks (%s)", who, why);
+  if (M == 0 || N == 0) return TPM_OK;
+  hipStream_t s = (hipStream_t)stream;
+  GemmParams p;
+  // few rows are bound by reading W: the tiles would multiply mostly padding
+  const bool rows = dtype == TPM_BF16 && !chunk_ready && M <= kRowsMax && N >= 8 && K >= 8;
+  SplitPlan pl;
+  if (!rows && !why) {
+    pl = planned_split(g);
+    const size_t need = plan_bytes(pl, M, N, num_chunks);
+    if (need > 0 && (!g.part || g.part_bytes < need)) pl = SplitPlan{};
+  }
+  make_params(g, pl, p);
+  p.bias = bias;
+  p.bias_f32 = bias_dtype == TPM_F32;
+  p.resid = residual;
+  p.ldr = ldr;
+  hipError_t e = hipSuccess;
+  if (rows) {
+    RangePlan r = plan_rows(M, N, K);
+    if (r.S > 1 && (!g.part || g.part_bytes < range_bytes(r, M, N))) r = ranges((K + kRowsStep - 1) / kRowsStep, 1);
+    p.splits = r.S;
+    p.ksteps_per_split = r.per;
+    p.partial = g.part;
+    e = launch_linear_rows(p, g.tb, s);
+  } else if (why) {
+    return run_any(g, p, s, who);
+  } else {
+    if (chunk_ready) e = launch_ctrl_init(ctrl, kCtrlWords, s);
+    if (e == hipSuccess) e = launch_linear(p, is_fp8(dtype), g.tb, tile_grid(p, s), s);
+  }
+  return e == hipSuccess ? TPM_OK : hip_fail(e, who);
+}
+
+int tp_linear_act_bwd(int64_t M, int64_t N, int64_t K,
+                      const void* X, int64_t ldx, const void* W, int64_t ldw,
+                      const void* Z, int64_t ldz, const void* dY, int64_t lddy, int dtype, int act,
+                      void* dW, int64_t lddw, int dw_dtype, void* dX, int64_t lddx, float* dbias,
+                      void* workspace, size_t workspace_bytes, void* stream) {
+  const char* who = "tp_linear_act_bwd";
+  if (M < 0 || N < 0 || K < 0) return fail(TPM_EINVAL, "%s: negative size", who);
+  if (M > INT32_MAX || N > INT32_MAX || K > INT32_MAX) return fail(TPM_EUNSUPPORTED, "%s: size >= 2^31", who);
+  if (!float_dt(dtype) || !float_dt(dw_dtype)) return fail(TPM_EINVAL, "%s: dtypes BF16 or F32", who);
+  if (dtype == TPM_F32 && dw_dtype != TPM_F32) return fail(TPM_EUNSUPPORTED, "%s: fp32 inputs give fp32 dW", who);
+  if (act < TPM_ACT_NONE || act > TPM_ACT_SILU) return fail(TPM_EINVAL, "%s: bad activation", who);
+  if (act == TPM_ACT_NONE) Z = nullptr;      // its derivative is 1
+  else if (!given(Z, M * N)) return fail(TPM_EINVAL, "%s: an activation needs Z (the saved pre-activation)", who);
+  if (!given(X, M * K) || !given(W, K * N) || !given(dY, M * N) || !given(dW, K * N) || !given(dX, M * K))
+    return fail(TPM_EINVAL, "%s: null pointer", who);
+  if (ldx < K || ldw < N || lddy < N || lddw < N || lddx < K || (Z && ldz < N))
+    return fail(TPM_EINVAL, "%s: leading dimension smaller than the row width", who);
+  const size_t need = tpm_workspace_bytes(TPM_OP_LINEAR_ACT_BWD, M, N, K, 1, 1, dtype);
+  if (!workspace || workspace_bytes < need) return fail(TPM_EWORKSPACE, "%s: workspace of %zu bytes required", who, need);
+  if (!aligned16(workspace)) return fail(TPM_EINVAL, "%s: workspace not 16-byte aligned", who);
+  hipStream_t s = (hipStream_t)stream;
+  uint32_t* ctrl = (uint32_t*)workspace;
+  char* at = (char*)workspace + kCtrlBytes;
+  void* dZ = at;
+  at += linear_dz_bytes(M, N, dtype);
+  float* bands = (float*)at;
+  at += linear_band_bytes(M, N);
+  float* part = (float*)at;
+  const size_t part_bytes = (size_t)((char*)workspace + workspace_bytes - at);
+  const void* dz = Z ? dZ : dY;
+  const int64_t lddz = Z ? N : lddy;
+  // dW = X^T dZ  [K, N] over M;  dX = dZ W^T  [M, K] over N
+  GemmDesc g_dw{K, N, M, X, ldx, true, dtype, nullptr, dz, lddz, false, dtype, nullptr,
+                dW, lddw, dw_dtype, TPM_EPI_FWD, TPM_ACT_NONE, nullptr, 0, nullptr,
+                1, nullptr, nullptr, nullptr, 0, ctrl, part, part_bytes};
+  GemmDesc g_dx{M, K, N, dz, lddz, false, dtype, nullptr, W, ldw, true, dtype, nullptr,
+                dX, lddx, dtype, TPM_EPI_FWD, TPM_ACT_NONE, nullptr, 0, nullptr,
+                1, nullptr, nullptr, nullptr, 0, ctrl, part, part_bytes};
+  hipError_t e = hipSuccess;
+  if (M > 0 && N > 0 && (Z || dbias)) {
+    const int nb = dact_bands(M, N);
+    e = launch_dact_columns(dY, lddy, Z, ldz, dtype == TPM_F32, act, M, N, Z ? dZ : nullptr, dbias ? bands : nullptr, nb, s);
+    if (e == hipSuccess && dbias) e = launch_column_sums(bands, nb, N, dbias, nullptr, s);
+  } else if (dbias && N > 0) {
+    e = launch_ctrl_init((uint32_t*)dbias, (int)N, s);   // the sum over no rows
+  }
+  if (e != hipSuccess) return hip_fail(e, who);
+  // The paired tile launch reads dW's operands MN-major, so any number of
+  // rows M will do there: only the other conditions of the fast path count.
+  GemmDesc f_dw = g_dw;
+  f_dw.K = (M + 7) / 8 * 8;
+  if (dtype == TPM_BF16 && M > 0 && N > 0 && K > 0 && !fast_path_blocker(f_dw) && !fast_path_blocker(g_dx)) {
+    int S[2];
+    plan_linear_bwd(M, N, K, dtype, S);
+    GemmParams p_dw, p_dx;
+    g_dx.part = (float*)((char*)part + partial_bytes(K, N, S[0]));
+    make_params(g_dw, SplitPlan{S[0]}, p_dw);
+    make_params(g_dx, SplitPlan{S[1]}, p_dx);
+    const int grid = std::max(8, std::min(stream_cus(s), p_dw.units + p_dx.units));
+    const int first = p_dx.ksteps_per_split > p_dw.ksteps_per_split ? 1 : 0;
+    e = launch_ctrl_init(ctrl + kCtrlQueue, 8, s);
+    if (e == hipSuccess) e = launch_gemm_pair_bf16(p_dw, false, false, p_dx, true, true, first, ctrl + kCtrlQueue, grid, s);
+    return e == hipSuccess ? TPM_OK : hip_fail(e, who);
+  }
+  for (GemmDesc* g : {&g_dw, &g_dx}) {
+    if (g->M == 0 || g->N == 0) continue;
+    GemmParams p;
+    make_params(*g, SplitPlan{}, p);
+    int rc = run_any(*g, p, s, who);
+    if (rc != TPM_OK) return rc;
+  }
+  return TPM_OK;
 }
 
 }  // extern "C"

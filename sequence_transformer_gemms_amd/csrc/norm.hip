@@ -19,7 +19,7 @@
 #include <algorithm>
 #include <type_traits>
 
-#include "tpm_device.hpp"
+#include "row_vec.hpp"
 #include "tpm_internal.hpp"
 
 namespace tpm {
@@ -29,14 +29,6 @@ namespace {
 // widest rows held in the registers of 1024 threads: 4 chunks of 8 each, 2 in
 // the backward, which also holds two column sums per column
 constexpr int64_t kNormMaxFwd = 32768, kNormMaxBwd = 16384;
-
-__device__ __forceinline__ float ld_f(const void* p, bool f32, int64_t i) {
-  return f32 ? ((const float*)p)[i] : bf16_to_f32(((const uint16_t*)p)[i]);
-}
-__device__ __forceinline__ void st_f(void* p, bool f32, int64_t i, float v) {
-  if (f32) ((float*)p)[i] = v;
-  else ((uint16_t*)p)[i] = f32_to_bf16_rne(v);
-}
 
 // Sum over the work-group (any whole number of waves up to 16), the same
 // value in every thread: shuffles within a wave, then the wave sums in wave
@@ -170,85 +162,6 @@ __global__ void __launch_bounds__(256) norm_bwd_any(const NormParams p) {
 // accesses), so rows of odd width or stride run here too: where D % 8 != 0
 // the row's last chunk is loaded from column D - 8, `shift` of its elements
 // belong to the chunk before it, are zeroed, and are not stored.
-typedef i32x4 i32x4_any __attribute__((aligned(2)));
-typedef f32x4 f32x4_any __attribute__((aligned(4)));
-typedef i32x2 i32x2_any __attribute__((aligned(1)));
-typedef uint32_t u32_any __attribute__((aligned(1)));
-
-template <bool F32>
-struct Raw8 {   // eight elements as loaded
-  i32x4 a, b;   // (b: fp32 only)
-};
-template <bool F32>
-__device__ __forceinline__ Raw8<F32> load8(const void* p, int64_t i) {
-  Raw8<F32> r;
-  if constexpr (F32) {
-    r.a = __builtin_bit_cast(i32x4, __builtin_nontemporal_load((const f32x4_any*)((const float*)p + i)));
-    r.b = __builtin_bit_cast(i32x4, __builtin_nontemporal_load((const f32x4_any*)((const float*)p + i + 4)));
-  } else {
-    r.a = __builtin_nontemporal_load((const i32x4_any*)((const uint16_t*)p + i));
-  }
-  return r;
-}
-template <bool F32>
-__device__ __forceinline__ void widen8(const Raw8<F32>& r, float (&v)[8]) {
-  if constexpr (F32) {
-#pragma unroll
-    for (int e = 0; e < 4; ++e) {
-      v[e] = __int_as_float(r.a[e]);
-      v[4 + e] = __int_as_float(r.b[e]);
-    }
-  } else {
-#pragma unroll
-    for (int e = 0; e < 4; ++e) {
-      v[2 * e] = __uint_as_float((uint32_t)r.a[e] << 16);
-      v[2 * e + 1] = __uint_as_float((uint32_t)r.a[e] & 0xFFFF0000u);
-    }
-  }
-}
-// gamma or bias: read again for every row, from the caches
-__device__ __forceinline__ void param8(const void* p, bool f32, int64_t i, float (&v)[8]) {
-  if (f32) {
-    const f32x4 a = *(const f32x4_any*)((const float*)p + i), b = *(const f32x4_any*)((const float*)p + i + 4);
-#pragma unroll
-    for (int e = 0; e < 4; ++e) {
-      v[e] = a[e];
-      v[4 + e] = b[e];
-    }
-  } else {
-    Raw8<false> r;
-    r.a = *(const i32x4_any*)((const uint16_t*)p + i);
-    widen8<false>(r, v);
-  }
-}
-template <bool F32>
-__device__ __forceinline__ void store8(void* p, int64_t i, const float (&v)[8], int shift) {
-  if (__builtin_expect(shift != 0, 0)) {
-#pragma unroll
-    for (int e = 1; e < 8; ++e)
-      if (e >= shift) st_f(p, F32, i + e, v[e]);
-    return;
-  }
-  if constexpr (F32) {
-    *(f32x4_any*)((float*)p + i) = f32x4{v[0], v[1], v[2], v[3]};
-    *(f32x4_any*)((float*)p + i + 4) = f32x4{v[4], v[5], v[6], v[7]};
-  } else {
-    i32x4 o;
-#pragma unroll
-    for (int e = 0; e < 4; ++e) o[e] = (int)pack_bf16x2(v[2 * e], v[2 * e + 1]);
-    *(i32x4_any*)((uint16_t*)p + i) = o;
-  }
-}
-__device__ __forceinline__ void codes8(uint8_t* p, const float (&y)[8], int shift) {
-  const uint32_t lo = fp8x4<false>(y[0], y[1], y[2], y[3]), hi = fp8x4<false>(y[4], y[5], y[6], y[7]);
-  if (__builtin_expect(shift != 0, 0)) {
-#pragma unroll
-    for (int e = 1; e < 8; ++e)
-      if (e >= shift) p[e] = (uint8_t)((e < 4 ? lo : hi) >> (8 * (e & 3)));
-    return;
-  }
-  *(i32x2_any*)p = i32x2{(int)lo, (int)hi};
-}
 // sum of the T partials of one chunk, fp32 in ascending t, four loads in flight
 template <bool F32>
 __device__ __forceinline__ void sum_partials(const NormParams& p, int64_t at, float (&v)[8]) {
@@ -496,25 +409,26 @@ __global__ void __launch_bounds__(1024) norm_bwd_vec(const NormParams p, int NT)
   }
 }
 
-// dgamma and dbias: the work-groups' partial column sums.  A work-group takes
-// 64 columns (a wave's lanes, 256 contiguous bytes of a row of partials); its
-// 16 waves add every 16th partial row each, and the wave sums are added in
-// wave order: a fixed order, and 256 work-groups at D = 8192 with both sums.
-__global__ void __launch_bounds__(1024) norm_bwd_columns(const NormParams p, int G) {
+// Column sums of fp32 partial rows: out0 of src [G, D], and out1 of the [G, D]
+// behind it (either may be null).  A work-group takes 64 columns (a wave's
+// lanes, 256 contiguous bytes of a partial row); its 16 waves add every 16th
+// row each, and the wave sums are added in wave order: a fixed order, and 256
+// work-groups at D = 8192 with both sums.
+__global__ void __launch_bounds__(1024) column_sums(const float* part, int G, int64_t D, float* out0, float* out1) {
   __shared__ float red[16][64];
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
   const int64_t c = (int64_t)blockIdx.x * 64 + lane;
-  const int which = p.dgamma ? blockIdx.y : 1;
-  float* out = which ? p.dbias : p.dgamma;
+  const bool second = blockIdx.y == 1 || !out0;
+  float* out = second ? out1 : out0;
   float s = 0.f;
-  if (c < p.D) {
-    const float* src = p.part + (int64_t)which * G * p.D + c;
+  if (c < D) {
+    const float* src = part + (second ? (int64_t)G * D : 0) + c;
 #pragma unroll 8
-    for (int g = wave; g < G; g += 16) s += src[(int64_t)g * p.D];
+    for (int g = wave; g < G; g += 16) s += src[(int64_t)g * D];
   }
   red[wave][lane] = s;
   __syncthreads();
-  if (wave == 0 && c < p.D) {
+  if (wave == 0 && c < D) {
     for (int w = 1; w < 16; ++w) s += red[w][lane];
     out[c] = s;
   }
@@ -593,9 +507,14 @@ hipError_t launch_norm_bwd(const NormParams& p, hipStream_t s) {
     });
   }
   hipError_t e = hipGetLastError();
-  if (e != hipSuccess || (!p.dgamma && !p.dbias)) return e;
-  const dim3 grid((unsigned)((p.D + 63) / 64), p.dgamma && p.dbias ? 2 : 1);
-  norm_bwd_columns<<<grid, 1024, 0, s>>>(p, G);
+  if (e != hipSuccess) return e;
+  return launch_column_sums(p.part, G, p.D, p.dgamma, p.dbias, s);
+}
+
+hipError_t launch_column_sums(const float* part, int G, int64_t D, float* out0, float* out1, hipStream_t s) {
+  if (D == 0 || (!out0 && !out1)) return hipSuccess;
+  const dim3 grid((unsigned)((D + 63) / 64), out0 && out1 ? 2 : 1);
+  column_sums<<<grid, 1024, 0, s>>>(part, G, D, out0, out1);
   return hipGetLastError();
 }
 

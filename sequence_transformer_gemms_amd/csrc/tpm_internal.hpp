@@ -62,6 +62,11 @@ struct GemmParams {
   int gu_off;                // gated epilogues: column offset of the up half in B / aux / Y (= N)
   int bn_out;                // output columns per tile (256; 128 for EPI_GATED)
   int16_t order[kMaxGroups];
+  // linear layer's forward: Y = act(acc * scale + bias) + resid
+  const void* bias;          // [N] or null
+  const void* resid;         // [M, ldr], type of Y, or null
+  int64_t ldr;
+  int bias_f32;
 };
 
 enum { EPI_FWD = 0, EPI_DACT = 1, EPI_GATED = 2, EPI_DGATED = 3 };
@@ -115,6 +120,26 @@ enum { NORM_Y_BF16 = 0, NORM_Y_F32 = 1, NORM_Y_E4M3 = 2, NORM_Y_MX = 3 };
 hipError_t launch_norm_fwd(const NormParams& p, hipStream_t s);
 hipError_t launch_norm_bwd(const NormParams& p, hipStream_t s);
 int norm_bwd_groups(int64_t rows, int64_t D);
+// out0, out1 [D] = column sums of the fp32 rows part[0 .. G) and part[G .. 2G) (either output may be null)
+hipError_t launch_column_sums(const float* part, int G, int64_t D, float* out0, float* out1, hipStream_t s);
+
+// The linear layer: Y = act(op(A) op(B) * scale + bias) + resid, aux the
+// pre-activation.
+// 256 x 256 tile program (gemm_linear.hip): operands of whole 16-byte chunks.
+hipError_t launch_linear(const GemmParams& p, bool fp8, bool w_kmajor, int grid, hipStream_t s);
+// Few rows, bf16 (linear_small.hip): 64-column strips times p.splits K ranges
+// of p.ksteps_per_split steps of 256, partial sums in p.partial.
+hipError_t launch_linear_rows(const GemmParams& p, bool w_kmajor, hipStream_t s);
+// Any shape, stride and alignment, bf16 or fp32 (linear_small.hip): 128 x 128
+// tiles times p.splits K ranges of p.ksteps_per_split steps of 128 bytes.
+hipError_t launch_linear_any(const GemmParams& p, bool trans_a, bool trans_b, hipStream_t s);
+constexpr int kRowsStep = 256, kRowsTile = 64, kRowsBlock = 16;
+constexpr int kAnyTile = 128;
+// dZ = dY * act'(Z) [M, N] (ld N; null: not stored, Z null: dZ = dY) and its
+// column sums per band of rows, part [bands, N] (null: none).
+hipError_t launch_dact_columns(const void* dY, int64_t lddy, const void* Z, int64_t ldz, bool f32, int act, int64_t M,
+                               int64_t N, void* dZ, float* part, int bands, hipStream_t s);
+int dact_bands(int64_t M, int64_t N);
 
 // kernels' launchers (return hipError_t of the launch)
 hipError_t launch_gemm_bf16(const GemmParams& p, bool a_kmajor, bool b_kmajor, int grid, hipStream_t s);
