@@ -332,39 +332,27 @@ def partial_reduce_seqshard(partials, out, *, T, rank, M=None, stream=None):
     return check(rc)
 
 
-class _on:
-    """The call's device made current for its launches, and the stream they go
-    to: the given one, else torch's current stream on the device that holds
-    the tensors.  Every tensor must be on that one GPU."""
+# torch's current stream on a device as an address; the long way round where
+# this torch has no such accessor
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
+    lambda device: torch.cuda.current_stream(device).cuda_stream)
 
-    __slots__ = ("stream", "guard")
 
-    def __init__(self, who, stream, *tensors):
-        dev = None
-        for t in tensors:
-            if t is None:
-                continue
-            if not t.is_cuda:
-                raise ValueError(f"{who}: tensors must be in GPU memory")
-            if dev is None:
-                dev = t.get_device()
-            elif t.get_device() != dev:
-                raise ValueError(f"{who}: tensors on different GPUs")
-        self.guard = None if dev == torch.cuda.current_device() else torch.cuda.device(dev)
-        if stream is None:
-            self.stream = torch.cuda.current_stream(dev).cuda_stream
-        else:
-            self.stream = stream if isinstance(stream, int) else stream.cuda_stream
-
-    def __enter__(self):
-        if self.guard is not None:
-            self.guard.__enter__()
-        return self.stream
-
-    def __exit__(self, *exc):
-        if self.guard is not None:
-            self.guard.__exit__(*exc)
-        return False
+def _call(who, fn, device, stream, *args):
+    """fn(*args, stream) on `device` (made current for the launches) and on
+    the given stream, else on torch's current stream of that device."""
+    if device < 0:
+        raise ValueError(f"{who}: tensors must be in GPU memory")
+    if stream is None:
+        st = _raw_stream(device)
+    else:
+        st = stream if isinstance(stream, int) else stream.cuda_stream
+    if device == torch.cuda.current_device():
+        rc = fn(*args, st)
+    else:
+        with torch.cuda.device(device):
+            rc = fn(*args, st)
+    return rc if rc == _abi.OK else check(rc)
 
 
 def _fresh_workspace(nbytes, like, stream):
@@ -376,39 +364,64 @@ def _fresh_workspace(nbytes, like, stream):
     return ws
 
 
-def _expect(who, name, t, shape, dtypes=None):
-    """t (or None) has this shape, a unit inner stride and one of the dtypes;
-    its address and row stride (0 for None and for vectors)."""
+def _expect(who, name, t, shape, dtypes, device):
+    """t (or None) has this shape, one of the dtypes, a unit inner stride, and
+    is on `device`: its address and row stride (0 for None and for vectors)."""
     if t is None:
         return None, 0
     if t.shape != shape:
         raise ValueError(f"{who}: {name} has shape {tuple(t.shape)}, not {tuple(shape)}")
-    if dtypes is not None and t.dtype not in dtypes:
+    if t.dtype not in dtypes:
         raise ValueError(f"{who}: {name} has dtype {t.dtype}")
-    n = len(shape)
-    if t.numel() == 0:   # (strides of an empty tensor say nothing)
-        return t.data_ptr(), (shape[-1] if n > 1 else 0)
-    if n and shape[-1] > 1 and t.stride(-1) != 1:
+    if t.get_device() != device:
+        raise ValueError(f"{who}: tensors on different devices ({name})")
+    if t.is_contiguous():   # (torch leaves the strides of empty tensors and of single rows arbitrary)
+        return t.data_ptr(), shape[-1]
+    stride = t.stride()
+    if stride[-1] != 1 and shape[-1] > 1:
         raise ValueError(f"{who}: {name} needs a unit inner stride")
-    if n < 2:
+    if len(shape) == 1:
         return t.data_ptr(), 0
-    # (the stride of a single row says nothing: torch leaves it arbitrary)
-    return t.data_ptr(), (t.stride(-2) if shape[-2] > 1 else shape[-1])
+    return t.data_ptr(), (stride[-2] if shape[-2] > 1 else shape[-1])
+
+
+def _expect_word(who, name, t, device):
+    """Address of one fp32 value on `device` (or None)."""
+    if t is None:
+        return None
+    if t.dtype != torch.float32 or t.numel() != 1:
+        raise ValueError(f"{who}: {name} is one fp32 value")
+    if t.get_device() != device:
+        raise ValueError(f"{who}: tensors on different devices ({name})")
+    return t.data_ptr()
+
+
+def _expect_bytes(who, name, t, device):
+    """Address and size of a contiguous byte tensor on `device`."""
+    if t.dtype != torch.uint8 or not t.is_contiguous():
+        raise ValueError(f"{who}: {name} is a contiguous uint8 tensor")
+    if t.get_device() != device:
+        raise ValueError(f"{who}: tensors on different devices ({name})")
+    return t.data_ptr(), t.numel()
 
 
 _FLOATS = (torch.bfloat16, torch.float32)
-_U8 = (torch.uint8,)
+_CODES = (torch.uint8, torch.float8_e4m3fn)
 _F32 = (torch.float32,)
 
 
-def _rows_partials(who, name, x):
+def _rows_partials(who, name, x, device):
     """x [rows, D], or [T, rows, D] partials -> (T, rows, D, address, partial stride, row stride)."""
-    if x.dim() not in (2, 3):
+    shape = x.shape
+    ptr, ld = _expect(who, name, x, shape, _FLOATS, device)
+    if len(shape) == 2:
+        return 1, shape[0], shape[1], ptr, 0, ld
+    if len(shape) != 3:
         raise ValueError(f"{who}: {name} is [rows, D], or [T, rows, D] partials")
-    ptr, ld = _expect(who, name, x, x.shape, _FLOATS)
-    if x.dim() == 2:
-        return 1, x.shape[0], x.shape[1], ptr, 0, ld
-    return x.shape[0], x.shape[1], x.shape[2], ptr, x.stride(0) if x.shape[0] > 1 else 0, ld
+    return shape[0], shape[1], shape[2], ptr, x.stride(0) if shape[0] > 1 else 0, ld
+
+
+_CODE = {torch.float32: F32, torch.bfloat16: BF16, torch.uint8: FP8_E4M3, torch.float8_e4m3fn: FP8_E4M3}
 
 
 def tp_rmsnorm_fwd(x, gamma, y, *, bias=None, residual=None, h=None, rstd=None, eps=1e-5, y_scale=None,
@@ -422,25 +435,24 @@ def tp_rmsnorm_fwd(x, gamma, y, *, bias=None, residual=None, h=None, rstd=None, 
     the step; amax_out gets max|y|) or with y_scales (MXFP8 block scales,
     mx_scales_bytes(rows, D) uint8)."""
     who = "tp_rmsnorm_fwd"
-    T, rows, D, xp, stride, ldx = _rows_partials(who, "x", x)
-    gp, _ = _expect(who, "gamma", gamma, (D,), _FLOATS)
-    bp, _ = _expect(who, "bias", bias, (D,), (gamma.dtype,))
-    rp, ldr = _expect(who, "residual", residual, (rows, D), _FLOATS)
-    hp, ldh = _expect(who, "h", h, (rows, D), _FLOATS if residual is None else (residual.dtype,))
-    rsp, _ = _expect(who, "rstd", rstd, (rows,), _F32)
-    yp, ldy = _expect(who, "y", y, (rows, D), (torch.bfloat16, torch.float32, torch.uint8))
-    if y_scales is not None and (y_scales.dtype != torch.uint8 or not y_scales.is_contiguous()
-                                 or y_scales.numel() < mx_scales_bytes(rows, D)):
-        raise ValueError(f"{who}: y_scales is a contiguous uint8 tensor of mx_scales_bytes({rows}, {D}) elements")
-    for name, t in (("y_scale", y_scale), ("amax_out", amax_out)):
-        if t is not None and (t.dtype != torch.float32 or t.numel() != 1):
-            raise ValueError(f"{who}: {name} is one fp32 value")
+    dev = x.get_device()
+    T, rows, D, xp, stride, ldx = _rows_partials(who, "x", x, dev)
+    gp, _ = _expect(who, "gamma", gamma, (D,), _FLOATS, dev)
+    bp, _ = _expect(who, "bias", bias, (D,), (gamma.dtype,), dev)
+    rp, ldr = _expect(who, "residual", residual, (rows, D), _FLOATS, dev)
+    hp, ldh = _expect(who, "h", h, (rows, D), _FLOATS if residual is None else (residual.dtype,), dev)
+    rsp, _ = _expect(who, "rstd", rstd, (rows,), _F32, dev)
+    yp, ldy = _expect(who, "y", y, (rows, D), _FLOATS + _CODES, dev)
+    ysp = None
+    if y_scales is not None:
+        ysp, n = _expect_bytes(who, "y_scales", y_scales, dev)
+        if n < mx_scales_bytes(rows, D):
+            raise ValueError(f"{who}: y_scales has fewer than mx_scales_bytes({rows}, {D}) elements")
     hdt = residual if residual is not None else h if h is not None else x
-    with _on(who, stream, x, gamma, y, bias, residual, h, rstd, y_scale, amax_out, y_scales) as st:
-        return check(lib.tp_rmsnorm_fwd(T, rows, D, xp, stride, ldx, dtype_code(x.dtype),
-                                        bp, gp, dtype_code(gamma.dtype), eps,
-                                        rp, ldr, hp, ldh, dtype_code(hdt.dtype), rsp,
-                                        yp, ldy, dtype_code(y.dtype), _ptr(y_scales), _ptr(y_scale), _ptr(amax_out), st))
+    return _call(who, lib.tp_rmsnorm_fwd, dev, stream, T, rows, D, xp, stride, ldx, _CODE[x.dtype],
+                 bp, gp, _CODE[gamma.dtype], eps, rp, ldr, hp, ldh, _CODE[hdt.dtype], rsp,
+                 yp, ldy, _CODE[y.dtype], ysp, _expect_word(who, "y_scale", y_scale, dev),
+                 _expect_word(who, "amax_out", amax_out, dev))
 
 
 def tp_rmsnorm_bwd(dy, h, rstd, gamma, dh, *, dres=None, dgamma=None, dbias=None, workspace=None, stream=None):
@@ -450,21 +462,21 @@ def tp_rmsnorm_bwd(dy, h, rstd, gamma, dh, *, dres=None, dgamma=None, dbias=None
     reaches h past the norm; dh [rows, D] the gradient of every addend of h;
     dgamma, dbias [D] fp32.  The workspace defaults to a fresh one."""
     who = "tp_rmsnorm_bwd"
-    T, rows, D, dyp, stride, lddy = _rows_partials(who, "dy", dy)
-    hp, ldh = _expect(who, "h", h, (rows, D), _FLOATS)
-    rsp, _ = _expect(who, "rstd", rstd, (rows,), _F32)
-    gp, _ = _expect(who, "gamma", gamma, (D,), _FLOATS)
-    rp, ldr = _expect(who, "dres", dres, (rows, D), (h.dtype,))
-    dhp, lddh = _expect(who, "dh", dh, (rows, D), _FLOATS)
-    dgp, _ = _expect(who, "dgamma", dgamma, (D,), _F32)
-    dbp, _ = _expect(who, "dbias", dbias, (D,), _F32)
-    with _on(who, stream, dy, h, rstd, gamma, dres, dh, dgamma, dbias, workspace) as st:
-        if workspace is None:
-            workspace = _fresh_workspace(workspace_bytes(OP_RMSNORM_BWD, rows, D, 0, T), dy, stream)
-        return check(lib.tp_rmsnorm_bwd(T, rows, D, dyp, stride, lddy, dtype_code(dy.dtype),
-                                        gp, dtype_code(gamma.dtype), hp, ldh, rsp, rp, ldr, dtype_code(h.dtype),
-                                        dhp, lddh, dtype_code(dh.dtype), dgp, dbp,
-                                        workspace.data_ptr(), workspace.numel(), st))
+    dev = dy.get_device()
+    T, rows, D, dyp, stride, lddy = _rows_partials(who, "dy", dy, dev)
+    hp, ldh = _expect(who, "h", h, (rows, D), _FLOATS, dev)
+    rsp, _ = _expect(who, "rstd", rstd, (rows,), _F32, dev)
+    gp, _ = _expect(who, "gamma", gamma, (D,), _FLOATS, dev)
+    rp, ldr = _expect(who, "dres", dres, (rows, D), (h.dtype,), dev)
+    dhp, lddh = _expect(who, "dh", dh, (rows, D), _FLOATS, dev)
+    dgp, _ = _expect(who, "dgamma", dgamma, (D,), _F32, dev)
+    dbp, _ = _expect(who, "dbias", dbias, (D,), _F32, dev)
+    if workspace is None:
+        workspace = _fresh_workspace(workspace_bytes(OP_RMSNORM_BWD, rows, D, 0, T), dy, stream)
+    wp, wn = _expect_bytes(who, "workspace", workspace, dev)
+    return _call(who, lib.tp_rmsnorm_bwd, dev, stream, T, rows, D, dyp, stride, lddy, _CODE[dy.dtype],
+                 gp, _CODE[gamma.dtype], hp, ldh, rsp, rp, ldr, _CODE[h.dtype],
+                 dhp, lddh, _CODE[dh.dtype], dgp, dbp, wp, wn)
 
 
 def tp_linear_fwd(X, W, Y, *, bias=None, residual=None, act=ACT_NONE, Z=None, trans_w=False, x_scale=None, w_scale=None,
@@ -474,31 +486,36 @@ def tp_linear_fwd(X, W, Y, *, bias=None, residual=None, act=ACT_NONE, Z=None, tr
     X [M, K], W [K, N] (trans_w: stored [N, K]) bf16, fp32, or uint8 e4m3
     codes with x_scale and w_scale (device fp32; W stored [N, K]); bias [N];
     residual, Z [M, N] of Y's dtype (Y may be residual); Y bf16 or fp32.  The
-    workspace defaults to a fresh one (pass one that is kept: tpm.alloc_workspace(
+    workspace defaults to a fresh one (or one that is kept: alloc_workspace(
     OP_LINEAR_FWD, M, N, K, 1, num_chunks, dtype_code(X.dtype)))."""
     who = "tp_linear_fwd"
     if X.dim() != 2 or W.dim() != 2:
         raise ValueError(f"{who}: X and W are matrices")
+    dev = X.get_device()
     M, K = X.shape
     N = W.shape[0] if trans_w else W.shape[1]
-    dtypes = _FLOATS + _U8 + (torch.float8_e4m3fn,)
-    xp, ldx = _expect(who, "X", X, (M, K), dtypes)
-    wp, ldw = _expect(who, "W", W, (N, K) if trans_w else (K, N), (X.dtype,))
-    yp, ldy = _expect(who, "Y", Y, (M, N), _FLOATS)
-    bp, _ = _expect(who, "bias", bias, (N,), _FLOATS)
-    rp, ldr = _expect(who, "residual", residual, (M, N), (Y.dtype,))
-    zp, ldz = _expect(who, "Z", Z, (M, N), (Y.dtype,))
-    for name, t in (("x_scale", x_scale), ("w_scale", w_scale)):
-        if t is not None and (t.dtype != torch.float32 or t.numel() != 1):
-            raise ValueError(f"{who}: {name} is one fp32 value")
-    code = dtype_code(X.dtype)
-    with _on(who, stream, X, W, Y, bias, residual, Z, x_scale, w_scale, chunk_ready, workspace) as st:
-        if workspace is None:
-            workspace = _fresh_workspace(workspace_bytes(OP_LINEAR_FWD, M, N, K, 1, num_chunks, code), X, stream)
-        return check(lib.tp_linear_fwd(M, N, K, xp, ldx, _ptr(x_scale), wp, ldw, int(trans_w), _ptr(w_scale), code,
-                                       bp, F32 if bias is None else dtype_code(bias.dtype), rp, ldr, act, zp, ldz, yp, ldy,
-                                       dtype_code(Y.dtype), num_chunks, _abi.int_array(chunk_order), _ptr(chunk_ready), epoch,
-                                       workspace.data_ptr(), workspace.numel(), st))
+    xp, ldx = _expect(who, "X", X, (M, K), _FLOATS + _CODES, dev)
+    wp, ldw = _expect(who, "W", W, (N, K) if trans_w else (K, N), (X.dtype,), dev)
+    yp, ldy = _expect(who, "Y", Y, (M, N), _FLOATS, dev)
+    bp, _ = _expect(who, "bias", bias, (N,), _FLOATS, dev)
+    rp, ldr = _expect(who, "residual", residual, (M, N), (Y.dtype,), dev)
+    zp, ldz = _expect(who, "Z", Z, (M, N), (Y.dtype,), dev)
+    code = _CODE[X.dtype]
+    cr = None
+    if chunk_ready is not None:
+        if chunk_ready.dtype not in (torch.int32, torch.uint32) or not chunk_ready.is_contiguous() \
+                or chunk_ready.numel() < num_chunks or chunk_ready.get_device() != dev:
+            raise ValueError(f"{who}: chunk_ready is num_chunks 32-bit words on the tensors' device")
+        cr = chunk_ready.data_ptr()
+    if chunk_order is not None and len(chunk_order) != num_chunks:
+        raise ValueError(f"{who}: chunk_order has {len(chunk_order)} entries, not num_chunks")
+    if workspace is None:
+        workspace = _fresh_workspace(workspace_bytes(OP_LINEAR_FWD, M, N, K, 1, num_chunks, code), X, stream)
+    kp, kn = _expect_bytes(who, "workspace", workspace, dev)
+    return _call(who, lib.tp_linear_fwd, dev, stream, M, N, K, xp, ldx, _expect_word(who, "x_scale", x_scale, dev),
+                 wp, ldw, int(trans_w), _expect_word(who, "w_scale", w_scale, dev), code,
+                 bp, F32 if bias is None else _CODE[bias.dtype], rp, ldr, act, zp, ldz, yp, ldy, _CODE[Y.dtype],
+                 num_chunks, _abi.int_array(chunk_order), cr, epoch, kp, kn)
 
 
 def tp_linear_act_bwd(X, W, dY, dW, dX, *, Z=None, act=ACT_NONE, dbias=None, workspace=None, stream=None):
@@ -509,23 +526,23 @@ def tp_linear_act_bwd(X, W, dY, dW, dX, *, Z=None, act=ACT_NONE, dbias=None, wor
     who = "tp_linear_act_bwd"
     if X.dim() != 2 or W.dim() != 2:
         raise ValueError(f"{who}: X and W are matrices")
+    dev = X.get_device()
     M, K = X.shape
     N = W.shape[1]
     same = (X.dtype,)
-    xp, ldx = _expect(who, "X", X, (M, K), _FLOATS)
-    wp, ldw = _expect(who, "W", W, (K, N), same)
-    yp, lddy = _expect(who, "dY", dY, (M, N), same)
-    zp, ldz = _expect(who, "Z", Z, (M, N), same)
-    dwp, lddw = _expect(who, "dW", dW, (K, N), _FLOATS)
-    dxp, lddx = _expect(who, "dX", dX, (M, K), same)
-    dbp, _ = _expect(who, "dbias", dbias, (N,), _F32)
-    code = dtype_code(X.dtype)
-    with _on(who, stream, X, W, dY, Z, dW, dX, dbias, workspace) as st:
-        if workspace is None:
-            workspace = _fresh_workspace(workspace_bytes(OP_LINEAR_ACT_BWD, M, N, K, 1, 1, code), X, stream)
-        return check(lib.tp_linear_act_bwd(M, N, K, xp, ldx, wp, ldw, zp, ldz, yp, lddy, code, act,
-                                           dwp, lddw, dtype_code(dW.dtype), dxp, lddx, dbp,
-                                           workspace.data_ptr(), workspace.numel(), st))
+    xp, ldx = _expect(who, "X", X, (M, K), _FLOATS, dev)
+    wp, ldw = _expect(who, "W", W, (K, N), same, dev)
+    yp, lddy = _expect(who, "dY", dY, (M, N), same, dev)
+    zp, ldz = _expect(who, "Z", Z, (M, N), same, dev)
+    dwp, lddw = _expect(who, "dW", dW, (K, N), _FLOATS, dev)
+    dxp, lddx = _expect(who, "dX", dX, (M, K), same, dev)
+    dbp, _ = _expect(who, "dbias", dbias, (N,), _F32, dev)
+    code = _CODE[X.dtype]
+    if workspace is None:
+        workspace = _fresh_workspace(workspace_bytes(OP_LINEAR_ACT_BWD, M, N, K, 1, 1, code), X, stream)
+    kp, kn = _expect_bytes(who, "workspace", workspace, dev)
+    return _call(who, lib.tp_linear_act_bwd, dev, stream, M, N, K, xp, ldx, wp, ldw, zp, ldz, yp, lddy, code, act,
+                 dwp, lddw, _CODE[dW.dtype], dxp, lddx, dbp, kp, kn)
 
 
 def signal_chunk(flag_tensor, index: int, value: int, stream=None):

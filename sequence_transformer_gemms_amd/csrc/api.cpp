@@ -5,6 +5,7 @@
 #include <algorithm>
 #include <cstdarg>
 #include <cstdio>
+#include <cmath>
 #include <cstring>
 #include <mutex>
 #include <vector>
@@ -188,36 +189,83 @@ void plan_linear_bwd(int64_t M, int64_t N, int64_t K, int dt, int (&S)[2]) {
   }
 }
 
-// ---- the linear layer's kernels beside the 256 x 256 tiles (linear_small.hip)
-struct RangePlan {
-  int S = 1, per = 1;        // K ranges, steps per range
+// ---- the linear layer's any-shape kernel (linear_small.hip)
+// Tile rows mb and K ranges S of `per` steps, by an estimate in us whose terms
+// were measured: a K step of a tile takes about step_us (a load's latency;
+// fp32: its MFMAs), longer where work-groups share a CU; B arrives at 5 TB/s
+// once about 450 work-groups ask for it, and each further row tile costs a
+// quarter of that again; S > 1 writes and reads S partial results at that rate
+// and adds a launch; the epilogue costs in proportion to the tile's rows.  Over
+// M 1 to 517, K 1003 to 8192, N 777 to 8192 the plan is within 10 % of the best
+// (mb, S) of a sweep.
+struct AnyPlan {
+  int mb = kAnyTile, S = 1, per = 1;
+  double us = 1e30;
 };
-RangePlan ranges(int64_t steps, int64_t S) {
-  RangePlan r;
-  steps = std::max<int64_t>(steps, 1);
-  S = std::max<int64_t>(1, std::min(S, steps));
-  r.per = (int)((steps + S - 1) / S);
-  r.S = (int)((steps + r.per - 1) / r.per);
-  return r;
+int64_t any_tiles(int64_t M, int64_t N, int mb) { return ((M + mb - 1) / mb) * ((N + kAnyTile - 1) / kAnyTile); }
+AnyPlan plan_any_tile(int64_t M, int64_t N, int64_t K, int dt, int mb, bool split = true) {
+  AnyPlan best;
+  best.mb = mb;
+  const int64_t tiles = any_tiles(M, N, mb);
+  const int64_t steps = std::max<int64_t>(1, (K * esize(dt) + kStepBytes - 1) / kStepBytes);
+  best.per = (int)std::min<int64_t>(steps, INT32_MAX);
+  if (tiles == 0) {
+    best.us = 0;
+    return best;
+  }
+  const bool f32 = dt == TPM_F32;
+  const double step_us = mb == 128 ? (f32 ? 2.0 : 1.1) : mb == 64 ? (f32 ? 1.1 : 0.75) : (f32 ? 0.7 : 0.6);
+  const double share = mb == 128 ? 0.6 : 0.7;
+  const double b_us = (double)K * (double)N * esize(dt) / 5e6 * (0.75 + 0.25 * (double)((M + mb - 1) / mb)), part_us = (double)M * (double)N * 8.0 / 5e6 + 0.02;
+  const int64_t max_s = split ? std::min<int64_t>((steps + 1) / 2, 64) : 1;
+  for (int64_t S = 1; S <= max_s; ++S) {
+    const int64_t per = (steps + S - 1) / S;
+    if (S > 1 && (steps + per - 1) / per != S) continue;
+    const double wgs = (double)tiles * (double)S;
+    const double run = (double)per * step_us * std::max(1.0, wgs / kPlanCUs * share);
+    const double us = std::max(run, b_us / std::min(1.0, wgs / 450.0)) + (S > 1 ? 3.0 + (double)S * part_us : 0.0) + mb * 0.012;
+    if (us < best.us) { best.us = us; best.S = (int)S; best.per = (int)per; }
+  }
+  return best;
 }
-// Few rows: about four work-groups per CU, so that the whole weight is in flight.
-constexpr int64_t kRowsMax = 64;
-RangePlan plan_rows(int64_t M, int64_t N, int64_t K) {
-  const int64_t tiles = ((N + kRowsTile - 1) / kRowsTile) * ((M + kRowsBlock - 1) / kRowsBlock);
-  return ranges((K + kRowsStep - 1) / kRowsStep, (1023 + tiles) / std::max<int64_t>(tiles, 1));
+AnyPlan plan_any(int64_t M, int64_t N, int64_t K, int dt, bool split = true) {
+  AnyPlan best;
+  for (int mb : {128, 64, 32}) {
+    const AnyPlan p = plan_any_tile(M, N, K, dt, mb, split);
+    if (p.us < best.us) best = p;
+    if (any_tiles(M, N, mb) >= 2 * kPlanCUs) break;   // the chip is full of this tile
+  }
+  return best;
 }
-// Any shape: K is cut where the 128 x 128 tiles leave CUs idle, two steps a range at least.
-RangePlan plan_any(int64_t M, int64_t N, int64_t K, int dt) {
-  const int64_t tiles = ((M + kAnyTile - 1) / kAnyTile) * ((N + kAnyTile - 1) / kAnyTile);
-  const int64_t steps = (K * esize(dt) + kStepBytes - 1) / kStepBytes;
-  if (tiles >= kPlanCUs || tiles == 0) return ranges(steps, 1);
-  return ranges(steps, std::min<int64_t>({(2 * kPlanCUs + tiles - 1) / tiles, std::max<int64_t>(1, steps / 2), 16}));
+// partial sums of the K ranges, whole tiles
+size_t range_bytes(const AnyPlan& p, int64_t M, int64_t N) {
+  return p.S > 1 ? (size_t)p.S * (size_t)any_tiles(M, N, p.mb) * p.mb * kAnyTile * 4 : 0;
 }
+// dW [K, N] over M and dX [M, K] over N share one launch, hence the tile rows.
+void plan_any_pair(int64_t M, int64_t N, int64_t K, int dt, AnyPlan (&out)[2]) {
+  double best = 1e30;
+  for (int mb : {128, 64, 32}) {
+    const AnyPlan w = plan_any_tile(K, N, M, dt, mb), x = plan_any_tile(M, K, N, dt, mb);
+    if (w.us + x.us < best) {
+      best = w.us + x.us;
+      out[0] = w;
+      out[1] = x;
+    }
+    if (any_tiles(K, N, mb) + any_tiles(M, K, mb) >= 2 * kPlanCUs) break;
+  }
+}
+// Whether the any-shape kernel serves a bf16 shape of whole chunks too: for few
+// rows W's traffic or the number of tiles bounds it, not the matrix cores (K
+// 8192, N 1280: M = 1 14 us, 29 on the 256 x 256 tiles, M = 256 23 and 33, M =
+// 512 35 both; N 8192: M = 1 25 and 32, M = 128 42 and 51, M = 256 71 and 63),
+// for small products the few tiles (1024^3: 21 us and 25).
+bool small_product(int64_t M, int64_t N, int64_t K) {
+  return (M <= 256 && M * N <= (int64_t)1 << 20) || (double)M * (double)N * (double)K <= (double)(1 << 30);
+}
+
 // workspace parts of the linear layer's backward: dZ, and dbias per band of rows
 size_t linear_dz_bytes(int64_t M, int64_t N, int dt) { return round_up((size_t)M * (size_t)N * (size_t)esize(dt), 256); }
 size_t linear_band_bytes(int64_t M, int64_t N) { return round_up((size_t)dact_bands(M, N) * (size_t)N * 4, 256); }
-size_t range_bytes(const RangePlan& r, int64_t M, int64_t N) { return partial_bytes(M, N, r.S); }
-
 struct GemmDesc {
   int64_t M, N, K;
   const void* A; int64_t lda; bool ta; int adt; const float* asc;
@@ -524,7 +572,6 @@ size_t tpm_workspace_bytes(int op, int64_t M, int64_t N, int64_t K, int T, int n
       return kCtrlBytes;
     case TPM_OP_LINEAR_FWD: {
       size_t part = plan_bytes(M, N, K, num_chunks, dtype);
-      if (dtype == TPM_BF16 && M <= kRowsMax) part = std::max(part, range_bytes(plan_rows(M, N, K), M, N));
       if (!is_fp8(dtype)) part = std::max(part, range_bytes(plan_any(M, N, K, dtype), M, N));
       return kCtrlBytes + part;
     }
@@ -532,7 +579,9 @@ size_t tpm_workspace_bytes(int op, int64_t M, int64_t N, int64_t K, int T, int n
       int S[2];
       plan_linear_bwd(M, N, K, dtype, S);
       const size_t pair = partial_bytes(K, N, S[0]) + partial_bytes(M, K, S[1]);
-      const size_t any = std::max(range_bytes(plan_any(K, N, M, dtype), K, N), range_bytes(plan_any(M, K, N, dtype), M, K));
+      AnyPlan p[2];
+      plan_any_pair(M, N, K, dtype, p);
+      const size_t any = range_bytes(p[0], K, N) + range_bytes(p[1], M, K);
       return kCtrlBytes + linear_dz_bytes(M, N, dtype) + linear_band_bytes(M, N) + std::max(pair, any);
     }
     case TPM_OP_RMSNORM_BWD:   // (rows, D): the work-groups' column sums of dgamma and dbias
@@ -766,16 +815,15 @@ int tile_grid(const GemmParams& p, hipStream_t s) {
   return std::min(grid, p.units);
 }
 
-// One product on the any-shape kernel, K cut where the scratch allows it.
-int run_any(const GemmDesc& g, GemmParams& p, hipStream_t s, const char* who) {
-  RangePlan r = plan_any(g.M, g.N, g.K, g.adt);
-  if (r.S > 1 && (!g.part || g.part_bytes < range_bytes(r, g.M, g.N)))
-    r = ranges((g.K * esize(g.adt) + kStepBytes - 1) / kStepBytes, 1);
+// The any-shape kernel's part of p under plan r, partial sums at `part`.
+void any_params(const AnyPlan& r, float* part, GemmParams& p) {
+  p.nt = (p.N + kAnyTile - 1) / kAnyTile;
+  p.mt_per_group = (p.M + r.mb - 1) / r.mb;
+  p.total_tiles = (int)any_tiles(p.M, p.N, r.mb);
   p.splits = r.S;
   p.ksteps_per_split = r.per;
-  p.partial = g.part;
-  hipError_t e = launch_linear_any(p, g.ta, g.tb, s);
-  return e == hipSuccess ? TPM_OK : hip_fail(e, who);
+  p.units = p.total_tiles * r.S;
+  p.partial = part;
 }
 
 }  // namespace
@@ -816,10 +864,9 @@ int tp_linear_fwd(int64_t M, int64_t N, int64_t K,
   if (M == 0 || N == 0) return TPM_OK;
   hipStream_t s = (hipStream_t)stream;
   GemmParams p;
-  // few rows are bound by reading W: the tiles would multiply mostly padding
-  const bool rows = dtype == TPM_BF16 && !chunk_ready && M <= kRowsMax && N >= 8 && K >= 8;
+  const bool any = why || (dtype == TPM_BF16 && !chunk_ready && small_product(M, N, K));
   SplitPlan pl;
-  if (!rows && !why) {
+  if (!any) {
     pl = planned_split(g);
     const size_t need = plan_bytes(pl, M, N, num_chunks);
     if (need > 0 && (!g.part || g.part_bytes < need)) pl = SplitPlan{};
@@ -830,19 +877,15 @@ int tp_linear_fwd(int64_t M, int64_t N, int64_t K,
   p.resid = residual;
   p.ldr = ldr;
   hipError_t e = hipSuccess;
-  if (rows) {
-    RangePlan r = plan_rows(M, N, K);
-    if (r.S > 1 && (!g.part || g.part_bytes < range_bytes(r, M, N))) r = ranges((K + kRowsStep - 1) / kRowsStep, 1);
-    p.splits = r.S;
-    p.ksteps_per_split = r.per;
-    p.partial = g.part;
-    e = launch_linear_rows(p, g.tb, s);
-  } else if (why) {
-    return run_any(g, p, s, who);
-  } else {
-    if (chunk_ready) e = launch_ctrl_init(ctrl, kCtrlWords, s);
-    if (e == hipSuccess) e = launch_linear(p, is_fp8(dtype), g.tb, tile_grid(p, s), s);
+  if (any) {
+    AnyPlan r = plan_any(M, N, K, dtype);
+    if (r.S > 1 && (!g.part || g.part_bytes < range_bytes(r, M, N))) r = plan_any(M, N, K, dtype, false);
+    any_params(r, g.part, p);
+    e = launch_linear_any(p, r.mb, g.tb, s);
+    return e == hipSuccess ? TPM_OK : hip_fail(e, who);
   }
+  if (chunk_ready) e = launch_ctrl_init(ctrl, kCtrlWords, s);
+  if (e == hipSuccess) e = launch_linear(p, is_fp8(dtype), g.tb, tile_grid(p, s), s);
   return e == hipSuccess ? TPM_OK : hip_fail(e, who);
 }
 
@@ -910,14 +953,16 @@ int tp_linear_act_bwd(int64_t M, int64_t N, int64_t K,
     if (e == hipSuccess) e = launch_gemm_pair_bf16(p_dw, false, false, p_dx, true, true, first, ctrl + kCtrlQueue, grid, s);
     return e == hipSuccess ? TPM_OK : hip_fail(e, who);
   }
-  for (GemmDesc* g : {&g_dw, &g_dx}) {
-    if (g->M == 0 || g->N == 0) continue;
-    GemmParams p;
-    make_params(*g, SplitPlan{}, p);
-    int rc = run_any(*g, p, s, who);
-    if (rc != TPM_OK) return rc;
-  }
-  return TPM_OK;
+  AnyPlan r[2];
+  plan_any_pair(M, N, K, dtype, r);
+  GemmParams p_dw, p_dx;
+  make_params(g_dw, SplitPlan{}, p_dw);
+  make_params(g_dx, SplitPlan{}, p_dx);
+  any_params(r[0], part, p_dw);      // (an empty product has no tiles, hence no units)
+  any_params(r[1], (float*)((char*)part + range_bytes(r[0], K, N)), p_dx);
+  if (p_dw.units + p_dx.units == 0) return TPM_OK;
+  e = launch_linear_any_pair(p_dw, p_dx, r[0].mb, s);
+  return e == hipSuccess ? TPM_OK : hip_fail(e, who);
 }
 
 }  // extern "C"

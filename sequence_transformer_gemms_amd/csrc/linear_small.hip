@@ -1,6 +1,6 @@
-// The linear layer's kernels beside the 256 x 256 tile program: few rows (a
-// decoding step), shapes and alignments that are no whole 16-byte chunks, fp32
-// on the matrix cores; and the elementwise part of its backward.
+// The linear layer's kernel beside the 256 x 256 tile program, for few rows (a
+// decoding step), shapes and alignments that are no whole 16-byte chunks, and
+// fp32; and the elementwise part of its backward.
 #include <algorithm>
 #include <type_traits>
 
@@ -18,185 +18,92 @@ __device__ __forceinline__ float scale_of(const GemmParams& p) {
   return s;
 }
 
-// Epilogue of one element: z = v + bias kept in aux, Y = act(z) + residual.
+// Four consecutive elements at i, of which n (1 .. 4) are inside the row.
+__device__ __forceinline__ f32x4 load4(const void* p, bool f32, int64_t i, int n) {
+  f32x4 v = {0.f, 0.f, 0.f, 0.f};
+  if (n == 4 && f32) return *(const f32x4_any*)((const float*)p + i);
+  if (n == 4) {
+    const i32x2 w = *(const i32x2_any*)((const uint16_t*)p + i);
+    return f32x4{__uint_as_float((uint32_t)w[0] << 16), __uint_as_float((uint32_t)w[0] & 0xFFFF0000u),
+                 __uint_as_float((uint32_t)w[1] << 16), __uint_as_float((uint32_t)w[1] & 0xFFFF0000u)};
+  }
+#pragma unroll
+  for (int e = 0; e < 3; ++e)
+    if (e < n) v[e] = ld_f(p, f32, i + e);
+  return v;
+}
+__device__ __forceinline__ void store4(void* p, bool f32, int64_t i, int n, const f32x4& v) {
+  if (n == 4 && f32) {
+    *(f32x4_any*)((float*)p + i) = v;
+  } else if (n == 4) {
+    *(i32x2_any*)((uint16_t*)p + i) = i32x2{(int)pack_bf16x2(v[0], v[1]), (int)pack_bf16x2(v[2], v[3])};
+  } else {
+#pragma unroll
+    for (int e = 0; e < 3; ++e)
+      if (e < n) st_f(p, f32, i + e, v[e]);
+  }
+}
+
+// Epilogue of four columns: z = v + bias kept in aux, Y = act(z) + residual r.
+__device__ __forceinline__ f32x4 bias4(const GemmParams& p, int64_t col) {
+  return p.bias ? load4(p.bias, p.bias_f32, col, (int)std::min<int64_t>(4, p.N - col)) : f32x4{0.f, 0.f, 0.f, 0.f};
+}
+__device__ __forceinline__ f32x4 resid4(const GemmParams& p, int64_t row, int64_t col) {
+  return p.resid ? load4(p.resid, p.y_f32, row * p.ldr + col, (int)std::min<int64_t>(4, p.N - col))
+                 : f32x4{0.f, 0.f, 0.f, 0.f};
+}
 template <int ACT>
-__device__ __forceinline__ void finish_one(const GemmParams& p, float v, int64_t row, int64_t col) {
-  if (p.bias) v += ld_f(p.bias, p.bias_f32, col);
-  if (p.aux) st_f(p.aux, p.aux_f32, row * p.ldaux + col, v);
-  v = act_fwd_c<ACT>(v);
-  if (p.resid) v += ld_f(p.resid, p.y_f32, row * p.ldr + col);
-  st_f(p.Y, p.y_f32, row * p.ldy + col, v);
+__device__ __forceinline__ void finish4(const GemmParams& p, f32x4 v, const f32x4& r, int64_t row, int64_t col) {
+  const int n = (int)std::min<int64_t>(4, p.N - col);
+  if (p.aux) store4(p.aux, p.aux_f32, row * p.ldaux + col, n, v);
+#pragma unroll
+  for (int e = 0; e < 4; ++e) v[e] = act_fwd_c<ACT>(v[e]);
+  store4(p.Y, p.y_f32, row * p.ldy + col, n, v + r);
 }
 
-// K-range partial sums [splits, M, N] added in ascending order, then the epilogue.
-__global__ void __launch_bounds__(256) finish_splits(const GemmParams p) {
+// Sums of the K ranges, then the epilogue.  The partial sums are laid out by
+// tile, part[range][tile][MB][128]; only the rows inside the matrix are written
+// and read.  A work-group takes one row of a tile: 32 threads for its 128
+// columns, times eight that add every eighth range (few dependent loads: a
+// decoding step has tens of ranges) and whose sums are added in order.
+template <int MB>
+__device__ __forceinline__ void finish_row(const GemmParams& p, int u, f32x4 (&red)[8][32]) {
+  const int q = threadIdx.x & 31, slice = threadIdx.x >> 5;
+  const int row = u / p.nt, strip = u - row * p.nt, tile = strip * p.mt_per_group + row / MB, col = strip * kAnyTile + 4 * q;
+  const f32x4* src = (const f32x4*)(p.partial + ((int64_t)tile * MB + row % MB) * kAnyTile) + q;
+  const int64_t range = (int64_t)p.total_tiles * MB * kAnyTile / 4;
+  f32x4 s = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll 4
+  for (int i = slice; i < p.splits; i += 8) s += src[i * range];
+  red[slice][q] = s;
   const float scale = scale_of(p);
-  const int64_t total = (int64_t)p.M * p.N;
-  with_act(p.act, [&](auto ac) {
-    constexpr int ACT = decltype(ac)::value;
-    for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < total; i += (int64_t)gridDim.x * 256) {
-      float s = 0.f;
-#pragma unroll 8
-      for (int sp = 0; sp < p.splits; ++sp) s += p.partial[sp * total + i];
-      const int64_t row = i / p.N;
-      finish_one<ACT>(p, s * scale, row, i - row * p.N);
-    }
-  });
-}
-
-// n (1 .. 7) elements at i, zeros behind them
-__device__ __forceinline__ i32x4 load_some(const uint16_t* p, int64_t i, int n) {
-  i32x4 w = {0, 0, 0, 0};
-#pragma unroll
-  for (int e = 0; e < 8; ++e)
-    if (e < n) w[e >> 1] |= (int)((uint32_t)p[i + e] << (16 * (e & 1)));
-  return w;
-}
-
-// --------------------------------------------------------------- few rows
-// Y of up to 16 rows at a time.  The weight is the traffic: each of its
-// 16-byte chunks is loaded once per 16 rows, straight into registers.  A
-// work-group of four waves owns 64 columns and a K range, 256 of K per step;
-// a lane holds 8 k x 8 columns of W per step (eight loads; a wave's loads
-// cover whole 128-byte lines in either layout of W) and for each row of X
-// reads its eight k from LDS and does 32 two-term dot products.  The lanes'
-// and waves' sums are joined at the end, the K ranges' by finish_splits.
-typedef __bf16 bf16x2v __attribute__((ext_vector_type(2)));
-__device__ __forceinline__ float dot2(uint32_t a, uint32_t b, float c) {
-  return __builtin_amdgcn_fdot2_f32_bf16(__builtin_bit_cast(bf16x2v, a), __builtin_bit_cast(bf16x2v, b), c, false);
-}
-
-template <int MT, bool WK>
-__global__ void __launch_bounds__(256) linear_rows(const GemmParams p) {
-  __shared__ __attribute__((aligned(16))) uint16_t xs[MT][kRowsStep];
-  __shared__ float red[4][MT][kRowsTile];
-  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-  const int n0 = blockIdx.x * kRowsTile, split = blockIdx.y, m0 = blockIdx.z * kRowsBlock;
-  const int rows = min(MT, p.M - m0);
-  const uint16_t* X = (const uint16_t*)p.A;
-  const uint16_t* W = (const uint16_t*)p.B;
-  const int steps = (p.K + kRowsStep - 1) / kRowsStep;
-  const int s0 = split * p.ksteps_per_split, s1 = min(steps, s0 + p.ksteps_per_split);
-  // this lane's 8 k (within the step) and its 8 columns: column cb + i
-  const int k_lane = 64 * wave + 8 * (WK ? lane & 7 : lane >> 3);
-  const int c_lane = 8 * (WK ? lane >> 3 : lane & 7);
-  const int cb = WK ? n0 + c_lane : min(n0 + c_lane, p.N - 8);   // (a last chunk of fewer columns is loaded from N - 8)
-  float acc[MT][8];
-#pragma unroll
-  for (int m = 0; m < MT; ++m)
-#pragma unroll
-    for (int i = 0; i < 8; ++i) acc[m][i] = 0.f;
-
-  auto load_w = [&](int s, i32x4 (&w)[8]) {
-    const int k = s * kRowsStep + k_lane;
-    if (s >= s1) return;
-    if ((s + 1) * kRowsStep <= p.K) {
-#pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        const int64_t at = WK ? (int64_t)min(cb + i, p.N - 1) * p.ldb + k : (int64_t)(k + i) * p.ldb + cb;
-        w[i] = __builtin_nontemporal_load((const i32x4_any*)(W + at));
-      }
-    } else {
-#pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        w[i] = i32x4{0, 0, 0, 0};
-        if constexpr (WK) {
-          const int n = min(8, p.K - k);
-          const int64_t at = (int64_t)min(cb + i, p.N - 1) * p.ldb + k;
-          if (n == 8) w[i] = __builtin_nontemporal_load((const i32x4_any*)(W + at));
-          else if (n > 0) w[i] = load_some(W, at, n);
-        } else {
-          if (k + i < p.K) w[i] = __builtin_nontemporal_load((const i32x4_any*)(W + (int64_t)(k + i) * p.ldb + cb));
-        }
-      }
-    }
-  };
-  auto load_x = [&](int s, uint16_t (&x)[MT]) {
-    const int k = s * kRowsStep + (int)threadIdx.x;
-#pragma unroll
-    for (int m = 0; m < MT; ++m) x[m] = (s < s1 && k < p.K && m < rows) ? X[(int64_t)(m0 + m) * p.lda + k] : (uint16_t)0;
-  };
-
-  i32x4 w[2][8];
-  uint16_t xr[MT];
-  load_x(s0, xr);
-  load_w(s0, w[0]);
-  auto step = [&](int s, i32x4 (&cur)[8], i32x4 (&next)[8]) {
-    __syncthreads();   // the previous step's reads of xs are done
-#pragma unroll
-    for (int m = 0; m < MT; ++m) xs[m][threadIdx.x] = xr[m];
-    __syncthreads();
-    load_x(s + 1, xr);
-    load_w(s + 1, next);
-    if constexpr (!WK) {
-      // (row 2j, row 2j + 1) pairs of each column, in place: cur[2j] takes
-      // columns 0-3, cur[2j + 1] columns 4-7
-#pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        const i32x4 a = cur[2 * j], b = cur[2 * j + 1];
-#pragma unroll
-        for (int h = 0; h < 4; ++h) {
-          const uint32_t lo = __builtin_amdgcn_perm((uint32_t)b[h], (uint32_t)a[h], 0x05040100u);
-          const uint32_t hi = __builtin_amdgcn_perm((uint32_t)b[h], (uint32_t)a[h], 0x07060302u);
-          if (h < 2) {
-            cur[2 * j][2 * h] = (int)lo;
-            cur[2 * j][2 * h + 1] = (int)hi;
-          } else {
-            cur[2 * j + 1][2 * h - 4] = (int)lo;
-            cur[2 * j + 1][2 * h - 3] = (int)hi;
-          }
-        }
-      }
-    }
-#pragma unroll
-    for (int m = 0; m < MT; ++m) {
-      const i32x4 x = *(const i32x4*)&xs[m][k_lane];
-#pragma unroll
-      for (int j = 0; j < 4; ++j)
-#pragma unroll
-        for (int i = 0; i < 8; ++i)
-          acc[m][i] = dot2((uint32_t)(WK ? cur[i][j] : cur[2 * j + (i >> 2)][i & 3]), (uint32_t)x[j], acc[m][i]);
-    }
-  };
-  for (int s = s0; s < s1; s += 2) {
-    step(s, w[0], w[1]);
-    if (s + 1 < s1) step(s + 1, w[1], w[0]);
-  }
-  // Sum over the eight lanes that share columns (they differ in three lane
-  // bits), halving the columns a lane keeps at each exchange.
-#pragma unroll
-  for (int m = 0; m < MT; ++m) {
-#pragma unroll
-    for (int b = 0; b < 3; ++b) {
-      const int bit = (WK ? 4 : 32) >> b, half = 4 >> b;
-      const bool up = (lane & bit) != 0;
-#pragma unroll
-      for (int i = 0; i < half; ++i) {
-        const float keep = up ? acc[m][i + half] : acc[m][i], give = up ? acc[m][i] : acc[m][i + half];
-        acc[m][i] = keep + __shfl_xor(give, bit, 64);
-      }
-    }
-    const int q = WK ? lane & 7 : lane >> 3;   // the column this lane kept
-    const int col = cb + q;
-    if (col >= n0 + c_lane) red[wave][m][col - n0] = acc[m][0];
-  }
   __syncthreads();
-  const float scale = scale_of(p);
-  for (int i = threadIdx.x; i < rows * kRowsTile; i += 256) {
-    const int m = i / kRowsTile, c = i - m * kRowsTile;
-    if (n0 + c >= p.N) continue;
-    const float s = ((red[0][m][c] + red[1][m][c]) + red[2][m][c]) + red[3][m][c];
-    if (p.splits > 1) p.partial[((int64_t)split * p.M + m0 + m) * p.N + n0 + c] = s;
-    else with_act(p.act, [&](auto ac) { finish_one<decltype(ac)::value>(p, s * scale, m0 + m, n0 + c); });
-  }
+  if (slice != 0 || col >= p.N) return;
+  const f32x4 bias = bias4(p, col), r = resid4(p, row, col);
+#pragma unroll
+  for (int i = 1; i < 8; ++i) s += red[i][q];
+  s = s * scale + bias;
+  with_act(p.act, [&](auto ac) { finish4<decltype(ac)::value>(p, s, r, row, col); });
+}
+template <int MB>
+__global__ void __launch_bounds__(256) finish_ranges(const GemmParams p) {
+  __shared__ f32x4 red[8][32];
+  finish_row<MB>(p, blockIdx.x, red);
+}
+// of two products: the first n0 work-groups are p0's
+template <int MB>
+__global__ void __launch_bounds__(256) finish_ranges_pair(const GemmParams p0, const GemmParams p1, int n0) {
+  __shared__ f32x4 red[8][32];
+  if ((int)blockIdx.x < n0) finish_row<MB>(p0, blockIdx.x, red);
+  else finish_row<MB>(p1, (int)blockIdx.x - n0, red);
 }
 
 // -------------------------------------------------------------- any shape
-// 128 x 128 tile per work-group of four waves (64 x 64 each, 2 x 2 MFMAs of
-// 32 x 32), K steps of 128 bytes (64 bf16, 32 fp32) through a double buffer in
-// LDS; the next step's chunks are loaded into registers while the current one
-// is multiplied.  Chunks of 16 bytes at any element address; what lies past an
-// edge is zero.  bf16: the LDS tiles keep each operand's order in memory
+// MB x 128 tile (MB = 128, 64 or 32 rows) per work-group of four waves, MFMAs
+// of 32 x 32, K steps of 128 bytes (64 bf16, 32 fp32) through a double buffer
+// in LDS; the next step's chunks are loaded into registers while the current
+// one is multiplied.  Chunks of 16 bytes at any element address; what lies
+// past an edge is zero.  bf16: the LDS tiles keep each operand's order in memory
 // (K-major rows of 128 bytes, MN-major rows of 256), and MN-major fragments
 // are transposed by the LDS read (ds_read_b64_tr_b16).  fp32
 // (v_mfma_f32_32x32x2_f32): a lane reads four k of its row at once and feeds
@@ -207,69 +114,95 @@ template <bool F32>
 struct AnyTile {
   static constexpr int E = F32 ? 4 : 8;             // elements of a chunk
   static constexpr int KS = F32 ? 32 : 64;          // K of a step
-  static constexpr int BYTES = kAnyTile * 128;      // LDS bytes of one operand tile
-  static constexpr int MN_CHUNKS = kAnyTile / E;    // chunks of an MN-major row
 };
 
-// LDS byte address of chunk c of row r: rows of 128 bytes (K-major) or of
-// MN_CHUNKS chunks (MN-major), swizzled so that the rows of one read differ
-// in their banks.
-template <bool F32, bool KM>
+// LDS byte address of chunk c of row r of an operand tile of ROWS rows: rows of
+// 128 bytes (K-major) or of ROWS / E chunks (MN-major), swizzled so that the
+// rows of one read differ in their banks.
+template <bool F32, bool KM, int ROWS>
 __device__ __forceinline__ uint32_t any_at(uint32_t r, uint32_t c) {
+  constexpr uint32_t RC = ROWS / AnyTile<F32>::E;
   if constexpr (KM) return r * 128u + ((c ^ ((r ^ (r >> 3)) & 7u)) << 4);
-  else return r * (AnyTile<F32>::MN_CHUNKS * 16u) + ((F32 ? c : c ^ ((r & 3u) << 2)) << 4);
+  else return r * (RC * 16u) + ((F32 ? c : c ^ (((r & 3u) << 2) & (RC - 1u))) << 4);
 }
 
-template <bool F32, bool KM>
-__device__ __forceinline__ void any_load(const void* base, int64_t ld, int mn0, int mn_end, int k0, int k_end,
-                                         i32x4 (&q)[4]) {
-  using T = AnyTile<F32>;
+// One thread's chunks of an operand tile of ROWS rows: ROWS / 32 of them, all
+// in the same columns of memory, chunk j a uniform distance behind the first.
+// K-major: operand rows line + 32 j, k from `first`; MN-major: k from line + j *
+// LINES, operand rows from `first`.  A chunk that crosses the row's end is loaded
+// so that it ends there and shifted into place when it is stored to LDS; rows
+// narrower than a chunk are gathered element by element.
+template <bool F32, bool KM, int ROWS>
+struct AnyOperand {
+  static constexpr int E = AnyTile<F32>::E, KS = AnyTile<F32>::KS, N = ROWS / 32, ESZ = F32 ? 4 : 2;
+  static constexpr int RC = KM ? 8 : ROWS / E;             // chunks of a tile's memory row
+  static constexpr int LINES = 256 / RC;                   // memory rows between chunks
+  const char* p;       // chunk 0 of step 0
+  int64_t ld;          // bytes
+  int line, first;     // of step 0
+  int lines, width;    // memory rows, and elements of a row
+  __device__ __forceinline__ AnyOperand(const void* base, int64_t ld_, int mn0, int mn_end, int K) {
+    line = (KM ? mn0 : 0) + (int)threadIdx.x / RC;
+    first = (KM ? 0 : mn0) + (int)threadIdx.x % RC * E;
+    lines = KM ? mn_end : K;
+    width = KM ? K : mn_end;
+    ld = ld_ * ESZ;
+    p = (const char*)base + line * ld + (int64_t)first * ESZ;
+  }
+  // elements of step s's chunks inside the row (more than E: all of them)
+  __device__ __forceinline__ int inside(int s) const { return width - first - (KM ? s * KS : 0); }
+  __device__ __forceinline__ void load(int s, i32x4 (&q)[N]) const {
+    const int l = line + (KM ? 0 : s * KS), n = inside(s);
+    const char* at = p + (KM ? (int64_t)s * 128 : (int64_t)s * KS * ld) - (n < E ? (E - n) * ESZ : 0);
 #pragma unroll
-  for (int j = 0; j < 4; ++j) {
-    const int P = j * 256 + (int)threadIdx.x;
-    int r, e, n;       // row in memory, first element of the chunk, elements of it inside
-    bool in;
-    if constexpr (KM) {
-      r = mn0 + (P >> 3);
-      e = k0 + (P & 7) * T::E;
-      n = k_end - e;
-      in = r < mn_end;
-    } else {
-      r = k0 + P / T::MN_CHUNKS;
-      e = mn0 + (P % T::MN_CHUNKS) * T::E;
-      n = mn_end - e;
-      in = r < k_end;
-    }
-    q[j] = i32x4{0, 0, 0, 0};
-    if (!in || n <= 0) continue;
-    const int64_t at = (int64_t)r * ld + e;
-    if (n >= T::E) {
-      if constexpr (F32) q[j] = __builtin_bit_cast(i32x4, *(const f32x4_any*)((const float*)base + at));
-      else q[j] = *(const i32x4_any*)((const uint16_t*)base + at);
-    } else if constexpr (F32) {
-#pragma unroll
-      for (int i = 0; i < 4; ++i)
-        if (i < n) q[j][i] = ((const int*)base)[at + i];
-    } else {
-      q[j] = load_some((const uint16_t*)base, at, n);
+    for (int j = 0; j < N; ++j) {
+      q[j] = i32x4{0, 0, 0, 0};
+      if (n <= 0 || l + j * LINES >= lines) continue;
+      if (width >= E) {
+        if constexpr (F32) q[j] = __builtin_bit_cast(i32x4, *(const f32x4_any*)(at + j * LINES * ld));
+        else q[j] = *(const i32x4_any*)(at + j * LINES * ld);
+      } else {   // (first = 0 here: the row is elements 0 .. n - 1)
+        uint64_t w[2] = {0, 0};
+#pragma unroll 1
+        for (int e = 0; e < n; ++e) {
+          const char* x = at + (E - n + e) * ESZ + j * LINES * ld;
+          const uint64_t v = F32 ? *(const uint32_t*)x : *(const uint16_t*)x;
+          w[e * ESZ >> 3] |= v << (e * ESZ * 8 & 63);
+        }
+        q[j] = i32x4{(int)w[0], (int)(w[0] >> 32), (int)w[1], (int)(w[1] >> 32)};
+      }
     }
   }
-}
-template <bool F32, bool KM>
-__device__ __forceinline__ void any_store(char* tile, const i32x4 (&q)[4]) {
+  __device__ __forceinline__ void store(int s, char* tile, i32x4 (&q)[N]) const {
+    const int n = inside(s);
+    if (__builtin_expect(n < E && n > 0 && width >= E, 0)) {
+      int bits = (E - n) * ESZ * 8;
 #pragma unroll
-  for (int j = 0; j < 4; ++j) {
-    const uint32_t P = (uint32_t)(j * 256 + (int)threadIdx.x);
-    const uint32_t r = KM ? P >> 3 : P / AnyTile<F32>::MN_CHUNKS, c = KM ? P & 7u : P % AnyTile<F32>::MN_CHUNKS;
-    *(i32x4*)(tile + any_at<F32, KM>(r, c)) = q[j];
+      for (int j = 0; j < N; ++j) {
+        uint64_t lo = (uint64_t)(uint32_t)q[j][0] | (uint64_t)(uint32_t)q[j][1] << 32;
+        uint64_t hi = (uint64_t)(uint32_t)q[j][2] | (uint64_t)(uint32_t)q[j][3] << 32;
+        const bool far = bits >= 64;
+        lo = far ? hi : lo;
+        hi = far ? 0 : hi;
+        const int b = bits & 63;
+        lo = (lo >> b) | (b ? hi << (64 - b) : 0);
+        hi >>= b;
+        q[j] = i32x4{(int)lo, (int)(lo >> 32), (int)hi, (int)(hi >> 32)};
+      }
+    }
+#pragma unroll
+    for (int j = 0; j < N; ++j) {
+      const uint32_t P = (uint32_t)(j * 256 + (int)threadIdx.x);
+      *(i32x4*)(tile + any_at<F32, KM, ROWS>(P / RC, P % RC)) = q[j];
+    }
   }
-}
+};
 // bf16: the 32 x 16 fragment of rows rb.., k 16 kk .. +15
-template <bool KM>
+template <bool KM, int ROWS>
 __device__ __forceinline__ bf16x8 any_frag(const char* tile, int rb, int kk) {
   const int lane = threadIdx.x & 63;
   if constexpr (KM) {
-    return *(const bf16x8*)(tile + any_at<false, true>((uint32_t)(rb + (lane & 31)), (uint32_t)(2 * kk + (lane >> 5))));
+    return *(const bf16x8*)(tile + any_at<false, true, ROWS>((uint32_t)(rb + (lane & 31)), (uint32_t)(2 * kk + (lane >> 5))));
   } else {
     const int g = lane >> 4, j = lane & 15;
     const uint32_t mn = (uint32_t)(rb + 16 * (g & 1) + 4 * (j & 3));
@@ -278,7 +211,7 @@ __device__ __forceinline__ bf16x8 any_frag(const char* tile, int rb, int kk) {
     for (int hh = 0; hh < 2; ++hh) {
       const uint32_t k = (uint32_t)(16 * kk + 8 * (g >> 1) + 4 * hh + (j >> 2));
       h[hh] = __builtin_amdgcn_ds_read_tr16_b64_v4i16(
-          (lds_i16x4_t*)((lds_void*)(tile + any_at<false, false>(k, mn >> 3) + 2u * (mn & 7u))));
+          (lds_i16x4_t*)((lds_void*)(tile + any_at<false, false, ROWS>(k, mn >> 3) + 2u * (mn & 7u))));
     }
     typedef short i16x8 __attribute__((ext_vector_type(8)));
     const i16x8 v = {h[0][0], h[0][1], h[0][2], h[0][3], h[1][0], h[1][1], h[1][2], h[1][3]};
@@ -286,105 +219,166 @@ __device__ __forceinline__ bf16x8 any_frag(const char* tile, int rb, int kk) {
   }
 }
 // fp32: row rb + lane % 32, k 8 q + 4 (lane / 32) + 0..3
-template <bool KM>
+template <bool KM, int ROWS>
 __device__ __forceinline__ f32x4 any_quad(const char* tile, int rb, int q) {
   const int lane = threadIdx.x & 63;
   const uint32_t r = (uint32_t)(rb + (lane & 31)), h = (uint32_t)(lane >> 5);
   if constexpr (KM) {
-    return *(const f32x4*)(tile + any_at<true, true>(r, 2u * (uint32_t)q + h));
+    return *(const f32x4*)(tile + any_at<true, true, ROWS>(r, 2u * (uint32_t)q + h));
   } else {
     f32x4 v;
 #pragma unroll
     for (uint32_t i = 0; i < 4; ++i)
-      v[i] = *(const float*)(tile + any_at<true, false>(8u * (uint32_t)q + 4u * h + i, r >> 2) + 4u * (r & 3u));
+      v[i] = *(const float*)(tile + any_at<true, false, ROWS>(8u * (uint32_t)q + 4u * h + i, r >> 2) + 4u * (r & 3u));
     return v;
   }
 }
 
-template <bool F32, bool AK, bool BK>
-__global__ void __launch_bounds__(256) linear_any(const GemmParams p, int nt) {
+// Where a strip has several row tiles, units of one XCD (work-group ids
+// congruent mod 8) are made contiguous in the logical order, in which the row
+// tiles follow each other: they read the same K range of the same columns of B
+// through that XCD's L2 (M 256, K 8192, N 1280: 24 -> 23 us, N 8192: 75 -> 71).
+// With one row tile B is read once anyway, and neighbouring strips at the same
+// time from neighbouring addresses (M = 1, N 8192: 25 us, 27 remapped).
+__device__ __forceinline__ int xcd_unit(const GemmParams& p, int i) {
+  const int per = p.units >> 3;
+  return p.mt_per_group > 1 && i < 8 * per ? (i & 7) * per + (i >> 3) : i;
+}
+
+// Unit u of p: K range u / tiles of tile u % tiles; tile t: row tile t % rows of
+// strip t / rows.
+template <int MB>
+constexpr int kAnyLds = 2 * (MB + kAnyTile) * 128;
+template <bool F32, bool AK, bool BK, int MB>
+__device__ __forceinline__ void any_unit(const GemmParams& p, int u, char* __restrict__ smem) {
   using T = AnyTile<F32>;
-  __shared__ __attribute__((aligned(1024))) char smem[2][2][T::BYTES];
+  // waves along N, and the 32 x 32 MFMA tiles of a wave
+  constexpr int WN = MB == 32 ? 4 : 2, FM = MB == 128 ? 2 : 1, FN = MB == 32 ? 1 : 2;
+  constexpr int A_BYTES = MB * 128, HALF = kAnyLds<MB> / 2;
+  static_assert(MB * kAnyTile * 4 <= kAnyLds<MB>, "the sums fit the staging block");
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-  const int m0 = (int)(blockIdx.x / nt) * kAnyTile, n0 = (int)(blockIdx.x % nt) * kAnyTile, split = blockIdx.y;
-  const int wm = (wave >> 1) * 64, wn = (wave & 1) * 64;
+  const int tiles = p.total_tiles, split = u / tiles, tile = u - split * tiles;
+  const int strip = tile / p.mt_per_group;
+  const int m0 = (tile - strip * p.mt_per_group) * MB, n0 = strip * kAnyTile;
+  const int wm = (wave / WN) * 32 * FM, wn = (wave % WN) * 32 * FN;
   const int steps = (p.K + T::KS - 1) / T::KS;
   const int s0 = split * p.ksteps_per_split, s1 = min(steps, s0 + p.ksteps_per_split);
-  f32x16 acc[2][2];
+  f32x16 acc[FM][FN];
 #pragma unroll
-  for (int i = 0; i < 2; ++i)
+  for (int i = 0; i < FM; ++i)
 #pragma unroll
-    for (int j = 0; j < 2; ++j)
+    for (int j = 0; j < FN; ++j)
 #pragma unroll
       for (int e = 0; e < 16; ++e) acc[i][j][e] = 0.f;
-  i32x4 qa[4], qb[4];
-  if (s0 < s1) {
-    any_load<F32, AK>(p.A, p.lda, m0, p.M, s0 * T::KS, p.K, qa);
-    any_load<F32, BK>(p.B, p.ldb, n0, p.N, s0 * T::KS, p.K, qb);
-  }
-  for (int s = s0; s < s1; ++s) {
-    char* ta = smem[(s - s0) & 1][0];
-    char* tb = smem[(s - s0) & 1][1];
-    any_store<F32, AK>(ta, qa);
-    any_store<F32, BK>(tb, qb);
+  // (two steps ahead: a step's multiplications are much shorter than a load)
+  i32x4 qa[2][MB / 32], qb[2][4];
+  const AnyOperand<F32, AK, MB> oa(p.A, p.lda, m0, p.M, p.K);
+  const AnyOperand<F32, BK, 128> ob(p.B, p.ldb, n0, p.N, p.K);
+  auto fetch = [&](int s, i32x4 (&a)[MB / 32], i32x4 (&b)[4]) {
+    if (s >= s1) return;
+    oa.load(s, a);
+    ob.load(s, b);
+  };
+  auto step = [&](int s, char* ta, i32x4 (&a_next)[MB / 32], i32x4 (&b_next)[4]) {
+    char* tb = ta + A_BYTES;
+    oa.store(s, ta, a_next);
+    ob.store(s, tb, b_next);
     // one barrier a step: a wave that stores into this buffer again, two
     // steps on, has passed the next step's barrier, before which every wave
     // finished reading it
     __syncthreads();
-    if (s + 1 < s1) {
-      any_load<F32, AK>(p.A, p.lda, m0, p.M, (s + 1) * T::KS, p.K, qa);
-      any_load<F32, BK>(p.B, p.ldb, n0, p.N, (s + 1) * T::KS, p.K, qb);
-    }
+    fetch(s + 2, a_next, b_next);
 #pragma unroll
     for (int kk = 0; kk < 4; ++kk) {
       if constexpr (F32) {
-        f32x4 a[2], b[2];
+        f32x4 a[FM], b[FN];
 #pragma unroll
-        for (int i = 0; i < 2; ++i) {
-          a[i] = any_quad<AK>(ta, wm + 32 * i, kk);
-          b[i] = any_quad<BK>(tb, wn + 32 * i, kk);
-        }
+        for (int i = 0; i < FM; ++i) a[i] = any_quad<AK, MB>(ta, wm + 32 * i, kk);
+#pragma unroll
+        for (int j = 0; j < FN; ++j) b[j] = any_quad<BK, 128>(tb, wn + 32 * j, kk);
 #pragma unroll
         for (int e = 0; e < 4; ++e)
 #pragma unroll
-          for (int i = 0; i < 2; ++i)
+          for (int i = 0; i < FM; ++i)
 #pragma unroll
-            for (int j = 0; j < 2; ++j)
-              acc[i][j] = __builtin_amdgcn_mfma_f32_32x32x2f32(b[j][e], a[i][e], acc[i][j], 0, 0, 0);
+            for (int j = 0; j < FN; ++j)
+              acc[i][j] = __builtin_amdgcn_mfma_f32_32x32x2f32(a[i][e], b[j][e], acc[i][j], 0, 0, 0);
       } else {
-        bf16x8 a[2], b[2];
+        bf16x8 a[FM], b[FN];
 #pragma unroll
-        for (int i = 0; i < 2; ++i) {
-          a[i] = any_frag<AK>(ta, wm + 32 * i, kk);
-          b[i] = any_frag<BK>(tb, wn + 32 * i, kk);
-        }
+        for (int i = 0; i < FM; ++i) a[i] = any_frag<AK, MB>(ta, wm + 32 * i, kk);
 #pragma unroll
-        for (int i = 0; i < 2; ++i)
+        for (int j = 0; j < FN; ++j) b[j] = any_frag<BK, 128>(tb, wn + 32 * j, kk);
 #pragma unroll
-          for (int j = 0; j < 2; ++j)
-            acc[i][j] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(b[j], a[i], acc[i][j], 0, 0, 0);
+        for (int i = 0; i < FM; ++i)
+#pragma unroll
+          for (int j = 0; j < FN; ++j)
+            acc[i][j] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(a[i], b[j], acc[i][j], 0, 0, 0);
       }
     }
+  };
+  fetch(s0, qa[0], qb[0]);
+  fetch(s0 + 1, qa[1], qb[1]);
+  for (int s = s0; s < s1; s += 2) {
+    step(s, smem, qa[0], qb[0]);
+    if (s + 1 < s1) step(s + 1, smem + HALF, qa[1], qb[1]);
   }
-  // lane l: row l % 32, columns 8 q + 4 (l / 32) + 0..3 of each 32 x 32 block
+  // Lane l holds column l % 32 and rows 8 q + 4 (l / 32) + 0..3 of each MFMA
+  // tile.  The sums go through LDS and one compact loop over rows of 128
+  // columns, four per thread: whole rows of 512 bytes in every store, and
+  // little code, which each work-group fetches to run once.
+  float* out = (float*)smem;
+  __syncthreads();
+#pragma unroll
+  for (int i = 0; i < FM; ++i)
+#pragma unroll
+    for (int j = 0; j < FN; ++j)
+#pragma unroll
+      for (int e = 0; e < 16; ++e)
+        out[(wm + 32 * i + 8 * (e >> 2) + 4 * (lane >> 5) + (e & 3)) * kAnyTile + wn + 32 * j + (lane & 31)] = acc[i][j][e];
+  __syncthreads();
+  const int quads = min(MB, p.M - m0) * (kAnyTile / 4);
+  if (p.splits > 1) {
+    f32x4* to = (f32x4*)(p.partial + (int64_t)u * (MB * kAnyTile));
+#pragma unroll 1
+    for (int i = threadIdx.x; i < quads; i += 256) to[i] = *(const f32x4*)(out + 4 * i);
+    return;
+  }
   const float scale = scale_of(p);
+  const int col = n0 + 4 * (threadIdx.x & 31);
+  if (col >= p.N) return;
+  const f32x4 bias = bias4(p, col);
   with_act(p.act, [&](auto ac) {
-    constexpr int ACT = decltype(ac)::value;
+    // (four rows at a time: the residual's loads are in flight together)
+#pragma unroll 1
+    for (int i = threadIdx.x; i < quads; i += 1024) {
+      f32x4 r[4];
 #pragma unroll
-    for (int i = 0; i < 2; ++i) {
-      const int row = m0 + wm + 32 * i + (lane & 31);
-      if (row >= p.M) continue;
+      for (int u = 0; u < 4; ++u)
+        if (i + 256 * u < quads) r[u] = resid4(p, m0 + (i >> 5) + 8 * u, col);
 #pragma unroll
-      for (int j = 0; j < 2; ++j)
-#pragma unroll
-        for (int e = 0; e < 16; ++e) {
-          const int col = n0 + wn + 32 * j + 8 * (e >> 2) + 4 * (lane >> 5) + (e & 3);
-          if (col >= p.N) continue;
-          if (p.splits > 1) p.partial[((int64_t)split * p.M + row) * p.N + col] = acc[i][j][e];
-          else finish_one<ACT>(p, acc[i][j][e] * scale, row, col);
-        }
+      for (int u = 0; u < 4; ++u)
+        if (i + 256 * u < quads)
+          finish4<decltype(ac)::value>(p, *(const f32x4*)(out + 4 * i + 1024 * u) * scale + bias, r[u],
+                                       m0 + (i >> 5) + 8 * u, col);
     }
   });
+}
+
+template <bool F32, bool BK, int MB>
+__global__ void __launch_bounds__(256, 2) linear_any(const GemmParams p) {
+  __shared__ __attribute__((aligned(1024))) char smem[kAnyLds<MB>];
+  any_unit<F32, true, BK, MB>(p, xcd_unit(p, blockIdx.x), smem);
+}
+
+// The two products of a linear layer's backward in one launch (both are short
+// where this kernel serves them): dW (p0, both operands MN-major), then dX (p1,
+// both K-major).
+template <bool F32, int MB>
+__global__ void __launch_bounds__(256, 2) linear_any_pair(const GemmParams p0, const GemmParams p1) {
+  __shared__ __attribute__((aligned(1024))) char smem[kAnyLds<MB>];
+  if ((int)blockIdx.x < p0.units) any_unit<F32, false, false, MB>(p0, xcd_unit(p0, blockIdx.x), smem);
+  else any_unit<F32, true, true, MB>(p1, xcd_unit(p1, (int)blockIdx.x - p0.units), smem);
 }
 
 // ---------------------------------------------------- backward, elementwise
@@ -397,14 +391,17 @@ __global__ void __launch_bounds__(256) dact_columns(const void* dY, int64_t lddy
                                                     int64_t M, int64_t N, int64_t band, void* dZ, float* part) {
   __shared__ float red[4][512];
   const int chunk = threadIdx.x & 63, sub = threadIdx.x >> 6;
-  const int64_t c0 = (int64_t)blockIdx.x * 512 + 8 * chunk;
-  const int n = (int)std::min<int64_t>(8, N - c0);       // columns of the chunk inside the matrix
+  int64_t c0 = (int64_t)blockIdx.x * 512 + 8 * chunk;
+  // a last chunk of fewer columns is loaded from N - 8: its first `shift`
+  // elements are the chunk's before it (rows of fewer than eight: one by one)
+  const int n = (int)std::min<int64_t>(8, N - c0), shift = N >= 8 && n > 0 ? 8 - n : 0;
   const int64_t r1 = std::min<int64_t>(M, (blockIdx.y + 1) * band);
   float sum[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+  c0 -= shift;
   with_act(act, [&](auto ac) {
     constexpr int ACT = decltype(ac)::value;
-    for (int64_t r = blockIdx.y * band + sub; r < r1; r += 4) {
-      if (n == 8) {
+    if (N >= 8 && n > 0) {
+      for (int64_t r = blockIdx.y * band + sub; r < r1; r += 4) {
         float g[8];
         const Raw8<F32> gy = load8<F32>(dY, r * lddy + c0);
         if (Z) {
@@ -414,29 +411,32 @@ __global__ void __launch_bounds__(256) dact_columns(const void* dY, int64_t lddy
           widen8<F32>(zz, z);
 #pragma unroll
           for (int e = 0; e < 8; ++e) g[e] *= act_grad_c<ACT>(z[e]);
-          store8<F32>(dZ, r * N + c0, g, 0);
+          store8<F32>(dZ, r * N + c0, g, shift);
         } else {
           widen8<F32>(gy, g);
         }
 #pragma unroll
         for (int e = 0; e < 8; ++e) sum[e] += g[e];
-      } else {
-#pragma unroll
-        for (int e = 0; e < 7; ++e) {
-          if (e >= n) continue;
-          float g = ld_f(dY, F32, r * lddy + c0 + e);
-          if (Z) {
-            g *= act_grad_c<ACT>(ld_f(Z, F32, r * ldz + c0 + e));
-            st_f(dZ, F32, r * N + c0 + e, g);
-          }
-          sum[e] += g;
+      }
+    } else if (chunk < n) {   // N < 8: thread `chunk` takes column `chunk`
+      for (int64_t r = blockIdx.y * band + sub; r < r1; r += 4) {
+        float g = ld_f(dY, F32, r * lddy + chunk);
+        if (Z) {
+          g *= act_grad_c<ACT>(ld_f(Z, F32, r * ldz + chunk));
+          st_f(dZ, F32, r * N + chunk, g);
         }
+        sum[0] += g;
       }
     }
   });
   if (!part) return;
+  if (N >= 8) {
 #pragma unroll
-  for (int e = 0; e < 8; ++e) red[sub][8 * chunk + e] = sum[e];
+    for (int e = 0; e < 8; ++e)
+      if (n > 0 && e >= shift) red[sub][8 * chunk + e - shift] = sum[e];
+  } else if (chunk < 8) {
+    red[sub][chunk] = sum[0];
+  }
   __syncthreads();
   for (int k = threadIdx.x; k < 512; k += 256) {
     const int64_t c = (int64_t)blockIdx.x * 512 + k;
@@ -444,44 +444,51 @@ __global__ void __launch_bounds__(256) dact_columns(const void* dY, int64_t lddy
   }
 }
 
-hipError_t launch_finish(const GemmParams& p, hipStream_t s) {
-  if (p.splits <= 1) return hipSuccess;
-  finish_splits<<<(int)std::min<int64_t>(((int64_t)p.M * p.N + 255) / 256, 8192), 256, 0, s>>>(p);
-  return hipGetLastError();
+template <class F>
+void with_tile(int mb, F&& f) {
+  if (mb == 32) f(std::integral_constant<int, 32>{});
+  else if (mb == 64) f(std::integral_constant<int, 64>{});
+  else f(std::integral_constant<int, kAnyTile>{});
 }
 
-template <bool WK>
-hipError_t rows_of(const GemmParams& p, hipStream_t s) {
-  const dim3 grid((p.N + kRowsTile - 1) / kRowsTile, p.splits, (p.M + kRowsBlock - 1) / kRowsBlock);
-  if (p.M <= 1) linear_rows<1, WK><<<grid, 256, 0, s>>>(p);
-  else if (p.M <= 2) linear_rows<2, WK><<<grid, 256, 0, s>>>(p);
-  else if (p.M <= 4) linear_rows<4, WK><<<grid, 256, 0, s>>>(p);
-  else if (p.M <= 8) linear_rows<8, WK><<<grid, 256, 0, s>>>(p);
-  else linear_rows<16, WK><<<grid, 256, 0, s>>>(p);
-  return hipGetLastError();
-}
-
-template <bool F32>
-hipError_t any_of(const GemmParams& p, bool ta, bool tb, hipStream_t s) {
-  const int nt = (p.N + kAnyTile - 1) / kAnyTile;
-  const dim3 grid((unsigned)(((p.M + kAnyTile - 1) / kAnyTile) * nt), p.splits);
-  if (!ta && tb) linear_any<F32, true, true><<<grid, 256, 0, s>>>(p, nt);
-  else if (!ta) linear_any<F32, true, false><<<grid, 256, 0, s>>>(p, nt);
-  else if (tb) linear_any<F32, false, true><<<grid, 256, 0, s>>>(p, nt);
-  else linear_any<F32, false, false><<<grid, 256, 0, s>>>(p, nt);
-  return hipGetLastError();
-}
+// work-groups of the finalisation: one per row and strip of 128 columns
+unsigned finish_groups(const GemmParams& p) { return p.splits > 1 ? (unsigned)p.M * (unsigned)p.nt : 0u; }
 
 }  // namespace
 
-hipError_t launch_linear_rows(const GemmParams& p, bool w_kmajor, hipStream_t s) {
-  hipError_t e = w_kmajor ? rows_of<true>(p, s) : rows_of<false>(p, s);
-  return e == hipSuccess ? launch_finish(p, s) : e;
+hipError_t launch_linear_any(const GemmParams& p, int mb, bool w_kmajor, hipStream_t s) {
+  hipError_t e = hipSuccess;
+  with_tile(mb, [&](auto mc) {
+    constexpr int MB = decltype(mc)::value;
+    if (p.a_dt == 0) {
+      if (w_kmajor) linear_any<true, true, MB><<<p.units, 256, 0, s>>>(p);
+      else linear_any<true, false, MB><<<p.units, 256, 0, s>>>(p);
+    } else {
+      if (w_kmajor) linear_any<false, true, MB><<<p.units, 256, 0, s>>>(p);
+      else linear_any<false, false, MB><<<p.units, 256, 0, s>>>(p);
+    }
+    e = hipGetLastError();
+    if (e != hipSuccess || p.splits <= 1) return;
+    finish_ranges<MB><<<finish_groups(p), 256, 0, s>>>(p);
+    e = hipGetLastError();
+  });
+  return e;
 }
 
-hipError_t launch_linear_any(const GemmParams& p, bool trans_a, bool trans_b, hipStream_t s) {
-  hipError_t e = p.a_dt == 0 ? any_of<true>(p, trans_a, trans_b, s) : any_of<false>(p, trans_a, trans_b, s);
-  return e == hipSuccess ? launch_finish(p, s) : e;
+hipError_t launch_linear_any_pair(const GemmParams& p_dw, const GemmParams& p_dx, int mb, hipStream_t s) {
+  hipError_t e = hipSuccess;
+  with_tile(mb, [&](auto mc) {
+    constexpr int MB = decltype(mc)::value;
+    const int grid = p_dw.units + p_dx.units;
+    if (p_dw.a_dt == 0) linear_any_pair<true, MB><<<grid, 256, 0, s>>>(p_dw, p_dx);
+    else linear_any_pair<false, MB><<<grid, 256, 0, s>>>(p_dw, p_dx);
+    e = hipGetLastError();
+    const unsigned n0 = finish_groups(p_dw), n1 = finish_groups(p_dx);
+    if (e != hipSuccess || n0 + n1 == 0) return;
+    finish_ranges_pair<MB><<<n0 + n1, 256, 0, s>>>(p_dw, p_dx, (int)n0);
+    e = hipGetLastError();
+  });
+  return e;
 }
 
 // Bands of rows of dact_columns: about 2048 work-groups, at least eight rows each.

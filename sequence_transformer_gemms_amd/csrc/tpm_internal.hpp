@@ -127,13 +127,13 @@ hipError_t launch_column_sums(const float* part, int G, int64_t D, float* out0, 
 // pre-activation.
 // 256 x 256 tile program (gemm_linear.hip): operands of whole 16-byte chunks.
 hipError_t launch_linear(const GemmParams& p, bool fp8, bool w_kmajor, int grid, hipStream_t s);
-// Few rows, bf16 (linear_small.hip): 64-column strips times p.splits K ranges
-// of p.ksteps_per_split steps of 256, partial sums in p.partial.
-hipError_t launch_linear_rows(const GemmParams& p, bool w_kmajor, hipStream_t s);
-// Any shape, stride and alignment, bf16 or fp32 (linear_small.hip): 128 x 128
-// tiles times p.splits K ranges of p.ksteps_per_split steps of 128 bytes.
-hipError_t launch_linear_any(const GemmParams& p, bool trans_a, bool trans_b, hipStream_t s);
-constexpr int kRowsStep = 256, kRowsTile = 64, kRowsBlock = 16;
+// Any shape, stride and alignment, bf16 or fp32 (linear_small.hip): p.total_tiles
+// tiles of mb (128, 64 or 32) x 128, p.nt of them in a row, times p.splits K
+// ranges of p.ksteps_per_split steps of 128 bytes = p.units work-groups; the
+// ranges' partial sums in p.partial (16-byte aligned).  A token-major.
+hipError_t launch_linear_any(const GemmParams& p, int mb, bool w_kmajor, hipStream_t s);
+// dW (both operands MN-major) and dX (both K-major) in one launch
+hipError_t launch_linear_any_pair(const GemmParams& p_dw, const GemmParams& p_dx, int mb, hipStream_t s);
 constexpr int kAnyTile = 128;
 // dZ = dY * act'(Z) [M, N] (ld N; null: not stored, Z null: dZ = dY) and its
 // column sums per band of rows, part [bands, N] (null: none).

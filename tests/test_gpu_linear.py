@@ -101,7 +101,7 @@ def fwd_check(M, N, K, dt=B, act=ops.ACT_NONE, trans_w=False, bias=True, res=Tru
     return Y
 
 
-# few rows: the kernel that streams W, every row count's variant, odd widths
+# few rows: every tile height, odd widths, K cut in many ranges
 ROWS = [(1, 8, 8), (1, 9, 11), (2, 64, 256), (3, 63, 257), (1, 1280, 8192), (4, 200, 1000), (5, 72, 2057), (8, 130, 520),
         (9, 8, 100), (16, 1288, 264), (17, 77, 300), (33, 264, 512), (64, 100, 1030), (1, 70, 8), (1, 4000, 16)]
 
@@ -115,7 +115,8 @@ def test_few_rows(M, N, K, trans_w):
 
 
 # whole 16-byte chunks: the 256 x 256 tiles, with split K, a tail split and ragged edges
-TILES = [(65, 264, 200), (300, 264, 200), (256, 256, 64), (520, 1288, 1024), (257, 8, 4096), (1000, 512, 8), (4352, 4096, 1024)]
+TILES = [(65, 264, 200), (300, 264, 200), (256, 256, 64), (520, 1288, 1024), (257, 8, 4096), (1000, 512, 8), (4352, 4096, 1024),
+         (1100, 1288, 1032), (2056, 520, 2048), (257, 4104, 2048)]
 
 
 @pytest.mark.parametrize("M,N,K", TILES)
@@ -131,8 +132,9 @@ def test_tiles(M, N, K, trans_w):
 @pytest.mark.parametrize("act", ACTS)
 @pytest.mark.parametrize("trans_w", [False, True])
 def test_tiles_every_activation(act, trans_w):
-    fwd_check(300, 520, 264, act=act, trans_w=trans_w)
-    fwd_check(300, 520, 264, act=act, trans_w=trans_w, res=False)
+    for M, N, K in ((300, 520, 264), (1100, 1288, 1032)):      # small products run on other tiles
+        fwd_check(M, N, K, act=act, trans_w=trans_w)
+        fwd_check(M, N, K, act=act, trans_w=trans_w, res=False)
 
 
 # anything else: odd sizes, offsets and strides, fp32
@@ -155,6 +157,8 @@ def test_small_fp32_and_narrow(M, N, K):
 
 def test_unaligned_arrays_of_whole_chunk_shapes():
     # sizes the tiles take, addresses and strides they do not
+    fwd_check(1100, 1288, 1032, off=1)
+    fwd_check(1100, 1288, 1032, ld=4, off=4)
     fwd_check(300, 264, 200, off=1)
     fwd_check(300, 264, 200, ld=4, off=4)
     fwd_check(300, 264, 200, ld=1)
@@ -171,7 +175,7 @@ def test_empty_contraction_and_empty_outputs():
     torch.cuda.synchronize()
 
 
-@pytest.mark.parametrize("M,N,K,dt", [(1, 264, 1000, B), (16, 100, 77, B), (300, 264, 200, B), (520, 1288, 1024, B), (129, 131, 67, B),
+@pytest.mark.parametrize("M,N,K,dt", [(1, 264, 1000, B), (16, 100, 77, B), (300, 264, 200, B), (520, 1288, 1024, B), (1100, 1288, 1032, B), (129, 131, 67, B),
                                       (129, 131, 67, F), (40, 264, 200, F)])
 @pytest.mark.parametrize("trans_w", [False, True])
 def test_integers_are_exact(M, N, K, dt, trans_w):
@@ -206,7 +210,7 @@ def test_fp8_operands(M, N, K):
 
 
 def test_residual_in_place():
-    for M, N, K in ((3, 264, 1000), (300, 264, 200), (520, 1288, 1024), (129, 131, 67)):
+    for M, N, K in ((3, 264, 1000), (300, 264, 200), (1100, 1288, 1032), (129, 131, 67)):
         fwd_check(M, N, K, inplace=True, act=ops.ACT_RELU)
 
 
@@ -228,7 +232,7 @@ def test_chunks_in_any_order_and_gated():
     assert all(torch.equal(outs[0], y) for y in outs[1:])
 
 
-@pytest.mark.parametrize("M,N,K", [(4, 264, 1000), (300, 264, 200), (129, 131, 67)])
+@pytest.mark.parametrize("M,N,K", [(4, 264, 1000), (300, 264, 200), (129, 131, 67), (1100, 1288, 1032)])
 @pytest.mark.parametrize("trans_w", [False, True])
 def test_infinities_and_nans_stay_in_their_row_and_column(M, N, K, trans_w):
     x, w = si.normal_f32((M, K), 95), si.normal_f32((K, N), 96, 0.05)
