@@ -365,10 +365,8 @@ def _fresh_workspace(nbytes, like, stream):
 
 
 def _expect(who, name, t, shape, dtypes, device):
-    """t (or None) has this shape, one of the dtypes, a unit inner stride, and
-    is on `device`: its address and row stride (0 for None and for vectors)."""
-    if t is None:
-        return None, 0
+    """t has this shape, one of the dtypes, a unit inner stride, and is on
+    `device`: its address and row stride."""
     if t.shape != shape:
         raise ValueError(f"{who}: {name} has shape {tuple(t.shape)}, not {tuple(shape)}")
     if t.dtype not in dtypes:
@@ -385,10 +383,11 @@ def _expect(who, name, t, shape, dtypes, device):
     return t.data_ptr(), (stride[-2] if shape[-2] > 1 else shape[-1])
 
 
+_ABSENT = (None, 0)
+
+
 def _expect_word(who, name, t, device):
-    """Address of one fp32 value on `device` (or None)."""
-    if t is None:
-        return None
+    """Address of one fp32 value on `device`."""
     if t.dtype != torch.float32 or t.numel() != 1:
         raise ValueError(f"{who}: {name} is one fp32 value")
     if t.get_device() != device:
@@ -407,6 +406,7 @@ def _expect_bytes(who, name, t, device):
 
 _FLOATS = (torch.bfloat16, torch.float32)
 _CODES = (torch.uint8, torch.float8_e4m3fn)
+_OPERANDS = _FLOATS + _CODES
 _F32 = (torch.float32,)
 
 
@@ -438,11 +438,11 @@ def tp_rmsnorm_fwd(x, gamma, y, *, bias=None, residual=None, h=None, rstd=None, 
     dev = x.get_device()
     T, rows, D, xp, stride, ldx = _rows_partials(who, "x", x, dev)
     gp, _ = _expect(who, "gamma", gamma, (D,), _FLOATS, dev)
-    bp, _ = _expect(who, "bias", bias, (D,), (gamma.dtype,), dev)
-    rp, ldr = _expect(who, "residual", residual, (rows, D), _FLOATS, dev)
-    hp, ldh = _expect(who, "h", h, (rows, D), _FLOATS if residual is None else (residual.dtype,), dev)
-    rsp, _ = _expect(who, "rstd", rstd, (rows,), _F32, dev)
-    yp, ldy = _expect(who, "y", y, (rows, D), _FLOATS + _CODES, dev)
+    bp, _ = _ABSENT if bias is None else _expect(who, "bias", bias, (D,), (gamma.dtype,), dev)
+    rp, ldr = _ABSENT if residual is None else _expect(who, "residual", residual, (rows, D), _FLOATS, dev)
+    hp, ldh = _ABSENT if h is None else _expect(who, "h", h, (rows, D), _FLOATS if residual is None else (residual.dtype,), dev)
+    rsp, _ = _ABSENT if rstd is None else _expect(who, "rstd", rstd, (rows,), _F32, dev)
+    yp, ldy = _expect(who, "y", y, (rows, D), _OPERANDS, dev)
     ysp = None
     if y_scales is not None:
         ysp, n = _expect_bytes(who, "y_scales", y_scales, dev)
@@ -451,8 +451,8 @@ def tp_rmsnorm_fwd(x, gamma, y, *, bias=None, residual=None, h=None, rstd=None, 
     hdt = residual if residual is not None else h if h is not None else x
     return _call(who, lib.tp_rmsnorm_fwd, dev, stream, T, rows, D, xp, stride, ldx, _CODE[x.dtype],
                  bp, gp, _CODE[gamma.dtype], eps, rp, ldr, hp, ldh, _CODE[hdt.dtype], rsp,
-                 yp, ldy, _CODE[y.dtype], ysp, _expect_word(who, "y_scale", y_scale, dev),
-                 _expect_word(who, "amax_out", amax_out, dev))
+                 yp, ldy, _CODE[y.dtype], ysp, None if y_scale is None else _expect_word(who, "y_scale", y_scale, dev),
+                 None if amax_out is None else _expect_word(who, "amax_out", amax_out, dev))
 
 
 def tp_rmsnorm_bwd(dy, h, rstd, gamma, dh, *, dres=None, dgamma=None, dbias=None, workspace=None, stream=None):
@@ -467,10 +467,10 @@ def tp_rmsnorm_bwd(dy, h, rstd, gamma, dh, *, dres=None, dgamma=None, dbias=None
     hp, ldh = _expect(who, "h", h, (rows, D), _FLOATS, dev)
     rsp, _ = _expect(who, "rstd", rstd, (rows,), _F32, dev)
     gp, _ = _expect(who, "gamma", gamma, (D,), _FLOATS, dev)
-    rp, ldr = _expect(who, "dres", dres, (rows, D), (h.dtype,), dev)
+    rp, ldr = _ABSENT if dres is None else _expect(who, "dres", dres, (rows, D), (h.dtype,), dev)
     dhp, lddh = _expect(who, "dh", dh, (rows, D), _FLOATS, dev)
-    dgp, _ = _expect(who, "dgamma", dgamma, (D,), _F32, dev)
-    dbp, _ = _expect(who, "dbias", dbias, (D,), _F32, dev)
+    dgp, _ = _ABSENT if dgamma is None else _expect(who, "dgamma", dgamma, (D,), _F32, dev)
+    dbp, _ = _ABSENT if dbias is None else _expect(who, "dbias", dbias, (D,), _F32, dev)
     if workspace is None:
         workspace = _fresh_workspace(workspace_bytes(OP_RMSNORM_BWD, rows, D, 0, T), dy, stream)
     wp, wn = _expect_bytes(who, "workspace", workspace, dev)
@@ -494,12 +494,12 @@ def tp_linear_fwd(X, W, Y, *, bias=None, residual=None, act=ACT_NONE, Z=None, tr
     dev = X.get_device()
     M, K = X.shape
     N = W.shape[0] if trans_w else W.shape[1]
-    xp, ldx = _expect(who, "X", X, (M, K), _FLOATS + _CODES, dev)
+    xp, ldx = _expect(who, "X", X, (M, K), _OPERANDS, dev)
     wp, ldw = _expect(who, "W", W, (N, K) if trans_w else (K, N), (X.dtype,), dev)
     yp, ldy = _expect(who, "Y", Y, (M, N), _FLOATS, dev)
-    bp, _ = _expect(who, "bias", bias, (N,), _FLOATS, dev)
-    rp, ldr = _expect(who, "residual", residual, (M, N), (Y.dtype,), dev)
-    zp, ldz = _expect(who, "Z", Z, (M, N), (Y.dtype,), dev)
+    bp, _ = _ABSENT if bias is None else _expect(who, "bias", bias, (N,), _FLOATS, dev)
+    rp, ldr = _ABSENT if residual is None else _expect(who, "residual", residual, (M, N), (Y.dtype,), dev)
+    zp, ldz = _ABSENT if Z is None else _expect(who, "Z", Z, (M, N), (Y.dtype,), dev)
     code = _CODE[X.dtype]
     cr = None
     if chunk_ready is not None:
@@ -512,10 +512,10 @@ def tp_linear_fwd(X, W, Y, *, bias=None, residual=None, act=ACT_NONE, Z=None, tr
     if workspace is None:
         workspace = _fresh_workspace(workspace_bytes(OP_LINEAR_FWD, M, N, K, 1, num_chunks, code), X, stream)
     kp, kn = _expect_bytes(who, "workspace", workspace, dev)
-    return _call(who, lib.tp_linear_fwd, dev, stream, M, N, K, xp, ldx, _expect_word(who, "x_scale", x_scale, dev),
-                 wp, ldw, int(trans_w), _expect_word(who, "w_scale", w_scale, dev), code,
+    return _call(who, lib.tp_linear_fwd, dev, stream, M, N, K, xp, ldx, None if x_scale is None else _expect_word(who, "x_scale", x_scale, dev),
+                 wp, ldw, int(trans_w), None if w_scale is None else _expect_word(who, "w_scale", w_scale, dev), code,
                  bp, F32 if bias is None else _CODE[bias.dtype], rp, ldr, act, zp, ldz, yp, ldy, _CODE[Y.dtype],
-                 num_chunks, _abi.int_array(chunk_order), cr, epoch, kp, kn)
+                 num_chunks, None if chunk_order is None else _abi.int_array(chunk_order), cr, epoch, kp, kn)
 
 
 def tp_linear_act_bwd(X, W, dY, dW, dX, *, Z=None, act=ACT_NONE, dbias=None, workspace=None, stream=None):
@@ -533,10 +533,10 @@ def tp_linear_act_bwd(X, W, dY, dW, dX, *, Z=None, act=ACT_NONE, dbias=None, wor
     xp, ldx = _expect(who, "X", X, (M, K), _FLOATS, dev)
     wp, ldw = _expect(who, "W", W, (K, N), same, dev)
     yp, lddy = _expect(who, "dY", dY, (M, N), same, dev)
-    zp, ldz = _expect(who, "Z", Z, (M, N), same, dev)
+    zp, ldz = _ABSENT if Z is None else _expect(who, "Z", Z, (M, N), same, dev)
     dwp, lddw = _expect(who, "dW", dW, (K, N), _FLOATS, dev)
     dxp, lddx = _expect(who, "dX", dX, (M, K), same, dev)
-    dbp, _ = _expect(who, "dbias", dbias, (N,), _F32, dev)
+    dbp, _ = _ABSENT if dbias is None else _expect(who, "dbias", dbias, (N,), _F32, dev)
     code = _CODE[X.dtype]
     if workspace is None:
         workspace = _fresh_workspace(workspace_bytes(OP_LINEAR_ACT_BWD, M, N, K, 1, 1, code), X, stream)

@@ -217,10 +217,9 @@ AnyPlan plan_any_tile(int64_t M, int64_t N, int64_t K, int dt, int mb, bool spli
   const double step_us = mb == 128 ? (f32 ? 2.0 : 1.1) : mb == 64 ? (f32 ? 1.1 : 0.75) : (f32 ? 0.7 : 0.6);
   const double share = mb == 128 ? 0.6 : 0.7;
   const double b_us = (double)K * (double)N * esize(dt) / 5e6 * (0.75 + 0.25 * (double)((M + mb - 1) / mb)), part_us = (double)M * (double)N * 8.0 / 5e6 + 0.02;
-  const int64_t max_s = split ? std::min<int64_t>((steps + 1) / 2, 64) : 1;
-  for (int64_t S = 1; S <= max_s; ++S) {
-    const int64_t per = (steps + S - 1) / S;
-    if (S > 1 && (steps + per - 1) / per != S) continue;
+  for (int64_t want : {1, 2, 3, 4, 6, 8, 12, 16, 24, 32, 48, 64}) {
+    if (want > 1 && (!split || want > (steps + 1) / 2)) break;
+    const int64_t per = (steps + want - 1) / want, S = (steps + per - 1) / per;
     const double wgs = (double)tiles * (double)S;
     const double run = (double)per * step_us * std::max(1.0, wgs / kPlanCUs * share);
     const double us = std::max(run, b_us / std::min(1.0, wgs / 450.0)) + (S > 1 ? 3.0 + (double)S * part_us : 0.0) + mb * 0.012;
