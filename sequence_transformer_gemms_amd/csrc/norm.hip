@@ -162,30 +162,25 @@ __global__ void __launch_bounds__(256) norm_bwd_any(const NormParams p) {
 // accesses), so rows of odd width or stride run here too: where D % 8 != 0
 // the row's last chunk is loaded from column D - 8, `shift` of its elements
 // belong to the chunk before it, are zeroed, and are not stored.
-// sum of the T partials of one chunk, fp32 in ascending t, four loads in flight
-template <bool F32>
+// v = the sum of the T partials of one chunk, fp32 in ascending t, up to B
+// loads in flight after the first
+template <bool F32, int B>
 __device__ __forceinline__ void sum_partials(const NormParams& p, int64_t at, float (&v)[8]) {
   widen8<F32>(load8<F32>(p.x, at), v);
-  int t = 1;
 #pragma unroll 1
-  for (; t + 3 < p.T; t += 4) {
-    Raw8<F32> q[4];
+  for (int t = 1; t < p.T; t += B) {
+    Raw8<F32> q[B];
 #pragma unroll
-    for (int k = 0; k < 4; ++k) q[k] = load8<F32>(p.x, at + (int64_t)(t + k) * p.x_stride);
+    for (int k = 0; k < B; ++k)
+      if (t + k < p.T) q[k] = load8<F32>(p.x, at + (int64_t)(t + k) * p.x_stride);
 #pragma unroll
-    for (int k = 0; k < 4; ++k) {
-      float w[8];
-      widen8<F32>(q[k], w);
+    for (int k = 0; k < B; ++k)
+      if (t + k < p.T) {
+        float w[8];
+        widen8<F32>(q[k], w);
 #pragma unroll
-      for (int e = 0; e < 8; ++e) v[e] += w[e];
-    }
-  }
-#pragma unroll 1
-  for (; t < p.T; ++t) {
-    float w[8];
-    widen8<F32>(load8<F32>(p.x, at + (int64_t)t * p.x_stride), w);
-#pragma unroll
-    for (int e = 0; e < 8; ++e) v[e] += w[e];
+        for (int e = 0; e < 8; ++e) v[e] += w[e];
+      }
   }
 }
 
@@ -245,7 +240,7 @@ __global__ void __launch_bounds__(1024, 4) norm_fwd_vec(const NormParams p, int 
       if (live && c >= 0) {
         Raw8<HF> rr;
         if (p.res) rr = load8<HF>(p.res, row * p.ldr + c);
-        sum_partials<XF>(p, row * p.ldx + c, v[u]);
+        sum_partials<XF, 4>(p, row * p.ldx + c, v[u]);
         if (p.bias) {
           float w[8];
           param8(p.bias, p.g_f32, c, w);
@@ -352,7 +347,7 @@ __global__ void __launch_bounds__(1024) norm_bwd_vec(const NormParams p, int NT)
         float g[8], x[8];
         hh[u] = load8<HF>(p.h, row * p.ldh + c);
         if (p.res) dres[u] = load8<HF>(p.res, row * p.ldr + c);
-        sum_partials<XF>(p, row * p.ldx + c, dy[u]);
+        sum_partials<XF, XF ? 2 : V == 1 ? 7 : 4>(p, row * p.ldx + c, dy[u]);
         param8(p.gamma, p.g_f32, c, g);
         drop(dy[u], shift);
         widen8<HF>(hh[u], x);
@@ -436,13 +431,15 @@ __global__ void __launch_bounds__(1024) column_sums(const float* part, int G, in
 
 }  // namespace
 
-// Work-groups of the backward.  Each sums its rows' column contributions, so
-// their number fixes the order of the column sums; it depends on the shape
-// alone, never on the stream or the arrays.  1024 threads per CU either way:
-// 512 work-groups of 512 threads where each sees eight rows or more (rows 8192,
-// D 8192: 100 us, 105 with 256 of 1024), 256 of 1024 below, where the partial
-// sums' own traffic counts (T = 8, rows 1024, D 8192: 45 us, 48 with 512).
-int norm_bwd_groups(int64_t rows, int64_t) { return (int)std::min<int64_t>(rows, rows >= 4096 ? 512 : 256); }
+// The most work-groups of the backward.  Each sums its rows' column
+// contributions, so their number fixes the order of the column sums; it depends
+// on the shape and the types alone, never on the stream or the arrays.  1024
+// threads per CU either way: 512 work-groups of 512 threads where each sees
+// eight rows or more (rows 8192, D 8192: 98 us, 104 with 256 of 1024), 256 of
+// 1024 where the partial sums' own traffic counts (T = 8, rows 1024, D 8192: 45
+// us and 48; rows 8192, D 16384: 201 and 210).
+static bool many_rows(int64_t rows, int64_t D) { return rows >= 4096 && D <= 8192; }
+int norm_bwd_groups(int64_t rows, int64_t D) { return (int)std::min<int64_t>(rows, many_rows(rows, D) ? 512 : 256); }
 
 // whole waves that cover D columns at V chunks of 8 a thread
 static int row_threads(int64_t D, int V) { return (int)((D + 512 * V - 1) / (512 * V)) * 64; }
@@ -492,14 +489,20 @@ hipError_t launch_norm_fwd(const NormParams& p, hipStream_t s) {
 }
 
 hipError_t launch_norm_bwd(const NormParams& p, hipStream_t s) {
-  const int G = norm_bwd_groups(p.rows, p.D);
+  int G = norm_bwd_groups(p.rows, p.D);
   if (p.D < 8 || p.D > kNormMaxBwd) {
     norm_bwd_any<<<G, 256, 0, s>>>(p);
   } else {
-    // two chunks per thread, one where fp32 arrays would spill its registers
-    const int V = (p.x_f32 || p.h_f32) && p.D <= 8192 ? 1 : 2;
+    // Two chunks per thread; one where that leaves the registers for all the
+    // loads of many partials, or where fp32 arrays would spill them (T = 8, rows
+    // 1024, D 8192: 45 us, 48 with two), and for few rows, which then get
+    // work-groups of their own (rows 100, D 8192: 12 us and 17).
+    const bool few = p.rows <= 256;
+    const int V = p.D <= 8192 && (p.x_f32 || p.h_f32 || p.T >= 4 || few) ? 1 : 2;
     const int NT = row_threads(p.D, V);
-    const int threads = std::max(1, (p.rows >= 4096 ? 512 : 1024) / NT) * NT;
+    const int slots = few ? 1 : std::max(1, (many_rows(p.rows, p.D) ? 512 : 1024) / NT);
+    G = (int)std::min<int64_t>(G, (p.rows + slots - 1) / slots);
+    const int threads = slots * NT;
     with_types(p, [&](auto xf, auto hf) {
       constexpr bool XF = decltype(xf)::value, HF = decltype(hf)::value;
       if (V == 1) norm_bwd_vec<XF, HF, 1><<<G, threads, 0, s>>>(p, NT);
