@@ -1016,6 +1016,31 @@ __device__ __forceinline__ void run_unit(const GemmParams& p, const Unit& un, ch
     constexpr int EPI_LD = LY::EPI_LD, EPI_COLS = LY::EPI_COLS, EPI_ROWS = LY::EPI_ROWS;
     constexpr int FPP = EPI_COLS / 32;                 // column fragments per pass
     constexpr int IPP = EPI_ROWS / 32;                 // row fragments per pass
+    // LIN: a pass's bf16 residual, one chunk of eight columns per group of
+    // eight rows, loaded for the first pass before its staging and for each
+    // later one while the pass before it is finished, so that only the first
+    // pass waits for memory (loads per group of four, each waited for: 1 to 3 %
+    // slower where K is 1024 to 2048.  A dword per line loaded ahead during the
+    // last K steps, to have the residual in the caches by then, made it worse)
+    constexpr int RG = LIN ? EPI_ROWS / 8 : 1;
+    [[maybe_unused]] i32x4 rq[2][RG];
+    [[maybe_unused]] const bool res16 = LIN && p.resid && !p.y_f32 && !raw;
+    auto load_residual = [&](auto pc) {
+      constexpr int pass = decltype(pc)::value;
+      if constexpr (LIN && pass < LY::PASSES) {
+        const int row0 = tl.m0 + wm + EPI_ROWS * (pass / LY::COL_PASSES) + (lane >> 3);
+        const int col = tl.n0 + wn + EPI_COLS * (pass % LY::COL_PASSES) + (lane & 7) * 8;
+        if (res16) {
+#pragma unroll
+          for (int g = 0; g < RG; ++g) {
+            rq[pass & 1][g] = i32x4{0, 0, 0, 0};
+            if (row0 + 8 * g < tl.m_end && col < p.N)
+              rq[pass & 1][g] = *(const i32x4*)((const uint16_t*)p.resid + (int64_t)(row0 + 8 * g) * p.ldr + col);
+          }
+        }
+      }
+    };
+    load_residual(IC<0>{});
     static_for<LY::PASSES>([&](auto pc) {
       constexpr int pass = decltype(pc)::value;
       constexpr int rp = pass / LY::COL_PASSES, cp = pass % LY::COL_PASSES;
@@ -1054,9 +1079,6 @@ __device__ __forceinline__ void run_unit(const GemmParams& p, const Unit& un, ch
         }
         });
       } else if constexpr (LIN) {
-        // groups of four rows per lane: the residual's loads and the staged
-        // values of a group are all issued before any is used
-        constexpr int GRP = 4;
         const int cl = (lane & 7) * 8;
         const int col = tl.n0 + wn + EPI_COLS * cp + cl;
         const int row00 = tl.m0 + wm + EPI_ROWS * rp + (lane >> 3);
@@ -1076,23 +1098,19 @@ __device__ __forceinline__ void run_unit(const GemmParams& p, const Unit& un, ch
           }
           return;
         }
+        load_residual(IC<pass + 1>{});
         float bias[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
         if (p.bias && col < p.N) load_oct(p.bias, 0, p.bias_f32, 0, col, bias);
         with_act(p.act, [&](auto ac) {
         constexpr int ACT = decltype(ac)::value;
         with_lk(p, [&](auto lkc) {
         constexpr int LK = decltype(lkc)::value;
-#pragma unroll 1
-        for (int it0 = 0; it0 < EPI_ROWS / 8; it0 += GRP) {
-          i32x4 rq[GRP];
+        constexpr bool RES = LK > 0 && (LK & LK_RES) != 0;
+        // groups of four rows per lane: the staged values of a group are read
+        // before any is used
+        constexpr int GRP = 4;
+        auto group = [&](int it0, const i32x4* r) {
           f32x4 v0s[GRP], v1s[GRP];
-#pragma unroll
-          for (int g = 0; g < GRP; ++g) {
-            rq[g] = i32x4{0, 0, 0, 0};
-            const int row = row00 + (it0 + g) * 8;
-            if (LK > 0 && (LK & LK_RES) != 0 && row < tl.m_end && col < p.N)
-              rq[g] = *(const i32x4*)((const uint16_t*)p.resid + (int64_t)row * p.ldr + col);
-          }
 #pragma unroll
           for (int g = 0; g < GRP; ++g) {
             const float* src = stage + ((it0 + g) * 8 + (lane >> 3)) * EPI_LD + cl;
@@ -1106,9 +1124,19 @@ __device__ __forceinline__ void run_unit(const GemmParams& p, const Unit& un, ch
             if (row < tl.m_end && col < p.N) {
               float v[8] = {v0[0] * scale, v0[1] * scale, v0[2] * scale, v0[3] * scale,
                             v1[0] * scale, v1[1] * scale, v1[2] * scale, v1[3] * scale};
-              lin_oct<ACT, LK>(p, v, bias, row, col, rq[g]);
+              if constexpr (RES) lin_oct<ACT, LK>(p, v, bias, row, col, r[g]);
+              else lin_oct<ACT, LK>(p, v, bias, row, col);
             }
           }
+        };
+        if constexpr (RES) {   // (unrolled: the residual's registers are indexed by constants)
+          static_for<EPI_ROWS / 8 / GRP>([&](auto gc) {
+            constexpr int g0 = decltype(gc)::value * GRP;
+            group(g0, &rq[pass & 1][g0]);
+          });
+        } else {
+#pragma unroll 1
+          for (int it0 = 0; it0 < EPI_ROWS / 8; it0 += GRP) group(it0, nullptr);
         }
         });
         });
