@@ -290,10 +290,12 @@ int tp_linear_bwd(int64_t M, int64_t N, int64_t K,
  * Chunks of X's rows, chunk_order, chunk_ready and epoch as in
  * seq_chunk_gemm.
  * Kernels: the 256 x 256 matrix-core tiles where seq_chunk_gemm's fast-path
- * conditions hold (bias and residual 16-byte aligned, ldr % 4 == 0); for BF16
- * products of few rows or little work, other BF16 shapes and alignments, and
- * F32, a matrix-core kernel of smaller tiles for any shape.  FP8_E4M3 and
- * chunk_ready need the fast-path conditions (TPM_EUNSUPPORTED otherwise).
+ * conditions hold (bias and residual 16-byte aligned, ldr % 4 == 0); for
+ * products of few rows or little work, other shapes and alignments, and F32, a
+ * matrix-core kernel of smaller tiles for any shape.  FP8_E4M3 weights are
+ * stored K-major (trans_w = 1); chunk_ready needs the fast-path conditions and
+ * takes the 256 x 256 tiles, whose sums may differ from the other kernel's in
+ * their order (TPM_EUNSUPPORTED otherwise).
  * workspace (16-byte aligned): required with chunk_ready; with
  * tpm_workspace_bytes(TPM_OP_LINEAR_FWD, M, N, K, 1, num_chunks, dtype) bytes
  * the contraction is split over idle CUs, with less or NULL it is not (the

@@ -253,13 +253,14 @@ void plan_any_pair(int64_t M, int64_t N, int64_t K, int dt, AnyPlan (&out)[2]) {
     if (any_tiles(K, N, mb) + any_tiles(M, K, mb) >= 2 * kPlanCUs) break;
   }
 }
-// Whether the any-shape kernel serves a bf16 shape of whole chunks too: for few
-// rows W's traffic or the number of tiles bounds it, not the matrix cores (K
-// 8192, N 1280: M = 1 14 us, 29 on the 256 x 256 tiles, M = 256 23 and 33, M =
-// 512 35 both; N 8192: M = 1 25 and 32, M = 128 42 and 51, M = 256 71 and 63),
-// for small products the few tiles (1024^3: 21 us and 25).
+// Whether the any-shape kernel serves a bf16 or e4m3 shape of whole chunks too:
+// for few rows W's traffic or the number of tiles bounds it, not the matrix
+// cores (K 8192, N 1280: M = 1 14 us, 29 on the 256 x 256 tiles, M = 256 23 and
+// 33, M = 512 35 both; N 8192: M = 1 25 and 32, M = 128 42 and 51, M = 256 71 and
+// 63), for small products the few large tiles (512^3 12 us and 27, 1024^3 17 and
+// 25, 2048 x 1024 x 1024 23 and 32, 2048 x 2048 x 1024 36 and 32).
 bool small_product(int64_t M, int64_t N, int64_t K) {
-  return (M <= 256 && M * N <= (int64_t)1 << 20) || (double)M * (double)N * (double)K <= (double)(1 << 30);
+  return (M <= 256 && M * N <= (int64_t)1 << 20) || (double)M * (double)N * (double)K <= 2.2e9;
 }
 
 // workspace parts of the linear layer's backward: dZ, and dbias per band of rows
@@ -571,7 +572,7 @@ size_t tpm_workspace_bytes(int op, int64_t M, int64_t N, int64_t K, int T, int n
       return kCtrlBytes;
     case TPM_OP_LINEAR_FWD: {
       size_t part = plan_bytes(M, N, K, num_chunks, dtype);
-      if (!is_fp8(dtype)) part = std::max(part, range_bytes(plan_any(M, N, K, dtype), M, N));
+      part = std::max(part, range_bytes(plan_any(M, N, K, dtype), M, N));
       return kCtrlBytes + part;
     }
     case TPM_OP_LINEAR_ACT_BWD: {
@@ -859,11 +860,11 @@ int tp_linear_fwd(int64_t M, int64_t N, int64_t K,
   if (!why && bias && !aligned16(bias)) why = "bias not 16-byte aligned";
   if (!why && residual && (!aligned16(residual) || ldr % 4 != 0)) why = "residual not 16-byte aligned or ldr % 4 != 0";
   if (why && chunk_ready) return fail(TPM_EUNSUPPORTED, "%s: chunk gating needs the matrix-core kernel (%s)", who, why);
-  if (why && is_fp8(dtype)) return fail(TPM_EUNSUPPORTED, "%s: fp8 operands need whole 16-byte chunks (%s)", who, why);
+  if (is_fp8(dtype) && !trans_w) return fail(TPM_EUNSUPPORTED, "%s: fp8 weights are stored K-major (trans_w = 1)", who);
   if (M == 0 || N == 0) return TPM_OK;
   hipStream_t s = (hipStream_t)stream;
   GemmParams p;
-  const bool any = why || (dtype == TPM_BF16 && !chunk_ready && small_product(M, N, K));
+  const bool any = why || (!chunk_ready && small_product(M, N, K));
   SplitPlan pl;
   if (!any) {
     pl = planned_split(g);
@@ -937,9 +938,13 @@ int tp_linear_act_bwd(int64_t M, int64_t N, int64_t K,
   if (e != hipSuccess) return hip_fail(e, who);
   // The paired tile launch reads dW's operands MN-major, so any number of
   // rows M will do there: only the other conditions of the fast path count.
+  // Up to about 8 GFLOP the any-shape kernel's smaller tiles fill the chip
+  // better (64 x 512 x 512 13 us and 32; 1024^3 28 and 46; 2048 x 1024 x 1024 42
+  // and 50; 2048^3 79 both; 8192 x 1280 x 1024 134 and 95).
   GemmDesc f_dw = g_dw;
   f_dw.K = (M + 7) / 8 * 8;
-  if (dtype == TPM_BF16 && M > 0 && N > 0 && K > 0 && !fast_path_blocker(f_dw) && !fast_path_blocker(g_dx)) {
+  const bool small = (double)M * (double)N * (double)K <= 2.2e9;
+  if (dtype == TPM_BF16 && !small && !fast_path_blocker(f_dw) && !fast_path_blocker(g_dx)) {
     int S[2];
     plan_linear_bwd(M, N, K, dtype, S);
     GemmParams p_dw, p_dx;

@@ -1,6 +1,6 @@
 // The linear layer's kernel beside the 256 x 256 tile program, for few rows (a
-// decoding step), shapes and alignments that are no whole 16-byte chunks, and
-// fp32; and the elementwise part of its backward.
+// decoding step), small products, shapes and alignments that are no whole
+// 16-byte chunks, and fp32; and the elementwise part of its backward.
 #include <algorithm>
 #include <type_traits>
 
@@ -100,7 +100,7 @@ __global__ void __launch_bounds__(256) finish_ranges_pair(const GemmParams p0, c
 
 // -------------------------------------------------------------- any shape
 // MB x 128 tile (MB = 128, 64 or 32 rows) per work-group of four waves, MFMAs
-// of 32 x 32, K steps of 128 bytes (64 bf16, 32 fp32) through a double buffer
+// of 32 x 32, K steps of 128 bytes (64 bf16, 32 fp32, 128 e4m3) through a double buffer
 // in LDS; the next step's chunks are loaded into registers while the current
 // one is multiplied.  Chunks of 16 bytes at any element address; what lies
 // past an edge is zero.  bf16: the LDS tiles keep each operand's order in memory
@@ -108,22 +108,26 @@ __global__ void __launch_bounds__(256) finish_ranges_pair(const GemmParams p0, c
 // are transposed by the LDS read (ds_read_b64_tr_b16).  fp32
 // (v_mfma_f32_32x32x2_f32): a lane reads four k of its row at once and feeds
 // four MFMAs; A and B agree on the order of k, which the sum does not mind.
+// e4m3 (v_mfma_f32_32x32x64_f8f6f4, both operands K-major) likewise.
 typedef __attribute__((address_space(3))) i16x4 lds_i16x4_t;
+typedef i32x4 i32x4_bytes __attribute__((aligned(1)));
 
-template <bool F32>
+enum { TY_F32 = 0, TY_BF16 = 1, TY_E4M3 = 2 };      // (the library's dtype codes)
+template <int TY>
 struct AnyTile {
-  static constexpr int E = F32 ? 4 : 8;             // elements of a chunk
-  static constexpr int KS = F32 ? 32 : 64;          // K of a step
+  static constexpr int ESZ = TY == TY_F32 ? 4 : TY == TY_BF16 ? 2 : 1;
+  static constexpr int E = 16 / ESZ;                // elements of a chunk
+  static constexpr int KS = 128 / ESZ;              // K of a step
 };
 
 // LDS byte address of chunk c of row r of an operand tile of ROWS rows: rows of
 // 128 bytes (K-major) or of ROWS / E chunks (MN-major), swizzled so that the
 // rows of one read differ in their banks.
-template <bool F32, bool KM, int ROWS>
+template <int TY, bool KM, int ROWS>
 __device__ __forceinline__ uint32_t any_at(uint32_t r, uint32_t c) {
-  constexpr uint32_t RC = ROWS / AnyTile<F32>::E;
+  constexpr uint32_t RC = ROWS / AnyTile<TY>::E;
   if constexpr (KM) return r * 128u + ((c ^ ((r ^ (r >> 3)) & 7u)) << 4);
-  else return r * (RC * 16u) + ((F32 ? c : c ^ (((r & 3u) << 2) & (RC - 1u))) << 4);
+  else return r * (RC * 16u) + ((TY == TY_F32 ? c : c ^ (((r & 3u) << 2) & (RC - 1u))) << 4);
 }
 
 // One thread's chunks of an operand tile of ROWS rows: ROWS / 32 of them, all
@@ -132,9 +136,9 @@ __device__ __forceinline__ uint32_t any_at(uint32_t r, uint32_t c) {
 // LINES, operand rows from `first`.  A chunk that crosses the row's end is loaded
 // so that it ends there and shifted into place when it is stored to LDS; rows
 // narrower than a chunk are gathered element by element.
-template <bool F32, bool KM, int ROWS>
+template <int TY, bool KM, int ROWS>
 struct AnyOperand {
-  static constexpr int E = AnyTile<F32>::E, KS = AnyTile<F32>::KS, N = ROWS / 32, ESZ = F32 ? 4 : 2;
+  static constexpr int E = AnyTile<TY>::E, KS = AnyTile<TY>::KS, ESZ = AnyTile<TY>::ESZ, N = ROWS / 32;
   static constexpr int RC = KM ? 8 : ROWS / E;             // chunks of a tile's memory row
   static constexpr int LINES = 256 / RC;                   // memory rows between chunks
   const char* p;       // chunk 0 of step 0
@@ -159,14 +163,13 @@ struct AnyOperand {
       q[j] = i32x4{0, 0, 0, 0};
       if (n <= 0 || l + j * LINES >= lines) continue;
       if (width >= E) {
-        if constexpr (F32) q[j] = __builtin_bit_cast(i32x4, *(const f32x4_any*)(at + j * LINES * ld));
-        else q[j] = *(const i32x4_any*)(at + j * LINES * ld);
+        q[j] = *(const i32x4_bytes*)(at + j * LINES * ld);
       } else {   // (first = 0 here: the row is elements 0 .. n - 1)
         uint64_t w[2] = {0, 0};
 #pragma unroll 1
         for (int e = 0; e < n; ++e) {
           const char* x = at + (E - n + e) * ESZ + j * LINES * ld;
-          const uint64_t v = F32 ? *(const uint32_t*)x : *(const uint16_t*)x;
+          const uint64_t v = ESZ == 4 ? *(const uint32_t*)x : ESZ == 2 ? *(const uint16_t*)x : *(const uint8_t*)x;
           w[e * ESZ >> 3] |= v << (e * ESZ * 8 & 63);
         }
         q[j] = i32x4{(int)w[0], (int)(w[0] >> 32), (int)w[1], (int)(w[1] >> 32)};
@@ -193,7 +196,7 @@ struct AnyOperand {
 #pragma unroll
     for (int j = 0; j < N; ++j) {
       const uint32_t P = (uint32_t)(j * 256 + (int)threadIdx.x);
-      *(i32x4*)(tile + any_at<F32, KM, ROWS>(P / RC, P % RC)) = q[j];
+      *(i32x4*)(tile + any_at<TY, KM, ROWS>(P / RC, P % RC)) = q[j];
     }
   }
 };
@@ -202,7 +205,7 @@ template <bool KM, int ROWS>
 __device__ __forceinline__ bf16x8 any_frag(const char* tile, int rb, int kk) {
   const int lane = threadIdx.x & 63;
   if constexpr (KM) {
-    return *(const bf16x8*)(tile + any_at<false, true, ROWS>((uint32_t)(rb + (lane & 31)), (uint32_t)(2 * kk + (lane >> 5))));
+    return *(const bf16x8*)(tile + any_at<TY_BF16, true, ROWS>((uint32_t)(rb + (lane & 31)), (uint32_t)(2 * kk + (lane >> 5))));
   } else {
     const int g = lane >> 4, j = lane & 15;
     const uint32_t mn = (uint32_t)(rb + 16 * (g & 1) + 4 * (j & 3));
@@ -211,7 +214,7 @@ __device__ __forceinline__ bf16x8 any_frag(const char* tile, int rb, int kk) {
     for (int hh = 0; hh < 2; ++hh) {
       const uint32_t k = (uint32_t)(16 * kk + 8 * (g >> 1) + 4 * hh + (j >> 2));
       h[hh] = __builtin_amdgcn_ds_read_tr16_b64_v4i16(
-          (lds_i16x4_t*)((lds_void*)(tile + any_at<false, false, ROWS>(k, mn >> 3) + 2u * (mn & 7u))));
+          (lds_i16x4_t*)((lds_void*)(tile + any_at<TY_BF16, false, ROWS>(k, mn >> 3) + 2u * (mn & 7u))));
     }
     typedef short i16x8 __attribute__((ext_vector_type(8)));
     const i16x8 v = {h[0][0], h[0][1], h[0][2], h[0][3], h[1][0], h[1][1], h[1][2], h[1][3]};
@@ -224,14 +227,24 @@ __device__ __forceinline__ f32x4 any_quad(const char* tile, int rb, int q) {
   const int lane = threadIdx.x & 63;
   const uint32_t r = (uint32_t)(rb + (lane & 31)), h = (uint32_t)(lane >> 5);
   if constexpr (KM) {
-    return *(const f32x4*)(tile + any_at<true, true, ROWS>(r, 2u * (uint32_t)q + h));
+    return *(const f32x4*)(tile + any_at<TY_F32, true, ROWS>(r, 2u * (uint32_t)q + h));
   } else {
     f32x4 v;
 #pragma unroll
     for (uint32_t i = 0; i < 4; ++i)
-      v[i] = *(const float*)(tile + any_at<true, false, ROWS>(8u * (uint32_t)q + 4u * h + i, r >> 2) + 4u * (r & 3u));
+      v[i] = *(const float*)(tile + any_at<TY_F32, false, ROWS>(8u * (uint32_t)q + 4u * h + i, r >> 2) + 4u * (r & 3u));
     return v;
   }
+}
+
+// e4m3, K-major: row rb + lane % 32, two chunks of 16 of the 64 k of half kk
+template <int ROWS>
+__device__ __forceinline__ i32x8 any_frag8(const char* tile, int rb, int kk) {
+  const int lane = threadIdx.x & 63;
+  const uint32_t r = (uint32_t)(rb + (lane & 31)), c = (uint32_t)(4 * kk + (lane >> 5));
+  const i32x4 lo = *(const i32x4*)(tile + any_at<TY_E4M3, true, ROWS>(r, c));
+  const i32x4 hi = *(const i32x4*)(tile + any_at<TY_E4M3, true, ROWS>(r, c + 2u));
+  return i32x8{lo[0], lo[1], lo[2], lo[3], hi[0], hi[1], hi[2], hi[3]};
 }
 
 // Where a strip has several row tiles, units of one XCD (work-group ids
@@ -249,9 +262,9 @@ __device__ __forceinline__ int xcd_unit(const GemmParams& p, int i) {
 // strip t / rows.
 template <int MB>
 constexpr int kAnyLds = 2 * (MB + kAnyTile) * 128;
-template <bool F32, bool AK, bool BK, int MB>
+template <int TY, bool AK, bool BK, int MB>
 __device__ __forceinline__ void any_unit(const GemmParams& p, int u, char* __restrict__ smem) {
-  using T = AnyTile<F32>;
+  using T = AnyTile<TY>;
   // waves along N, and the 32 x 32 MFMA tiles of a wave
   constexpr int WN = MB == 32 ? 4 : 2, FM = MB == 128 ? 2 : 1, FN = MB == 32 ? 1 : 2;
   constexpr int A_BYTES = MB * 128, HALF = kAnyLds<MB> / 2;
@@ -272,8 +285,8 @@ __device__ __forceinline__ void any_unit(const GemmParams& p, int u, char* __res
       for (int e = 0; e < 16; ++e) acc[i][j][e] = 0.f;
   // (two steps ahead: a step's multiplications are much shorter than a load)
   i32x4 qa[2][MB / 32], qb[2][4];
-  const AnyOperand<F32, AK, MB> oa(p.A, p.lda, m0, p.M, p.K);
-  const AnyOperand<F32, BK, 128> ob(p.B, p.ldb, n0, p.N, p.K);
+  const AnyOperand<TY, AK, MB> oa(p.A, p.lda, m0, p.M, p.K);
+  const AnyOperand<TY, BK, 128> ob(p.B, p.ldb, n0, p.N, p.K);
   auto fetch = [&](int s, i32x4 (&a)[MB / 32], i32x4 (&b)[4]) {
     if (s >= s1) return;
     oa.load(s, a);
@@ -289,8 +302,19 @@ __device__ __forceinline__ void any_unit(const GemmParams& p, int u, char* __res
     __syncthreads();
     fetch(s + 2, a_next, b_next);
 #pragma unroll
-    for (int kk = 0; kk < 4; ++kk) {
-      if constexpr (F32) {
+    for (int kk = 0; kk < (TY == TY_E4M3 ? 2 : 4); ++kk) {
+      if constexpr (TY == TY_E4M3) {
+        i32x8 a[FM], b[FN];
+#pragma unroll
+        for (int i = 0; i < FM; ++i) a[i] = any_frag8<MB>(ta, wm + 32 * i, kk);
+#pragma unroll
+        for (int j = 0; j < FN; ++j) b[j] = any_frag8<128>(tb, wn + 32 * j, kk);
+#pragma unroll
+        for (int i = 0; i < FM; ++i)
+#pragma unroll
+          for (int j = 0; j < FN; ++j)
+            acc[i][j] = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(a[i], b[j], acc[i][j], 0, 0, 0, 0, 0, 0);
+      } else if constexpr (TY == TY_F32) {
         f32x4 a[FM], b[FN];
 #pragma unroll
         for (int i = 0; i < FM; ++i) a[i] = any_quad<AK, MB>(ta, wm + 32 * i, kk);
@@ -365,20 +389,20 @@ __device__ __forceinline__ void any_unit(const GemmParams& p, int u, char* __res
   });
 }
 
-template <bool F32, bool BK, int MB>
+template <int TY, bool BK, int MB>
 __global__ void __launch_bounds__(256, 2) linear_any(const GemmParams p) {
   __shared__ __attribute__((aligned(1024))) char smem[kAnyLds<MB>];
-  any_unit<F32, true, BK, MB>(p, xcd_unit(p, blockIdx.x), smem);
+  any_unit<TY, true, BK, MB>(p, xcd_unit(p, blockIdx.x), smem);
 }
 
 // The two products of a linear layer's backward in one launch (both are short
 // where this kernel serves them): dW (p0, both operands MN-major), then dX (p1,
 // both K-major).
-template <bool F32, int MB>
+template <int TY, int MB>
 __global__ void __launch_bounds__(256, 2) linear_any_pair(const GemmParams p0, const GemmParams p1) {
   __shared__ __attribute__((aligned(1024))) char smem[kAnyLds<MB>];
-  if ((int)blockIdx.x < p0.units) any_unit<F32, false, false, MB>(p0, xcd_unit(p0, blockIdx.x), smem);
-  else any_unit<F32, true, true, MB>(p1, xcd_unit(p1, (int)blockIdx.x - p0.units), smem);
+  if ((int)blockIdx.x < p0.units) any_unit<TY, false, false, MB>(p0, xcd_unit(p0, blockIdx.x), smem);
+  else any_unit<TY, true, true, MB>(p1, xcd_unit(p1, (int)blockIdx.x - p0.units), smem);
 }
 
 // ---------------------------------------------------- backward, elementwise
@@ -460,12 +484,15 @@ hipError_t launch_linear_any(const GemmParams& p, int mb, bool w_kmajor, hipStre
   hipError_t e = hipSuccess;
   with_tile(mb, [&](auto mc) {
     constexpr int MB = decltype(mc)::value;
-    if (p.a_dt == 0) {
-      if (w_kmajor) linear_any<true, true, MB><<<p.units, 256, 0, s>>>(p);
-      else linear_any<true, false, MB><<<p.units, 256, 0, s>>>(p);
+    if (p.a_dt == TY_E4M3) {
+      if (!w_kmajor) { e = hipErrorInvalidValue; return; }  // rejected on the host first
+      linear_any<TY_E4M3, true, MB><<<p.units, 256, 0, s>>>(p);
+    } else if (p.a_dt == TY_F32) {
+      if (w_kmajor) linear_any<TY_F32, true, MB><<<p.units, 256, 0, s>>>(p);
+      else linear_any<TY_F32, false, MB><<<p.units, 256, 0, s>>>(p);
     } else {
-      if (w_kmajor) linear_any<false, true, MB><<<p.units, 256, 0, s>>>(p);
-      else linear_any<false, false, MB><<<p.units, 256, 0, s>>>(p);
+      if (w_kmajor) linear_any<TY_BF16, true, MB><<<p.units, 256, 0, s>>>(p);
+      else linear_any<TY_BF16, false, MB><<<p.units, 256, 0, s>>>(p);
     }
     e = hipGetLastError();
     if (e != hipSuccess || p.splits <= 1) return;
@@ -480,8 +507,8 @@ hipError_t launch_linear_any_pair(const GemmParams& p_dw, const GemmParams& p_dx
   with_tile(mb, [&](auto mc) {
     constexpr int MB = decltype(mc)::value;
     const int grid = p_dw.units + p_dx.units;
-    if (p_dw.a_dt == 0) linear_any_pair<true, MB><<<grid, 256, 0, s>>>(p_dw, p_dx);
-    else linear_any_pair<false, MB><<<grid, 256, 0, s>>>(p_dw, p_dx);
+    if (p_dw.a_dt == TY_F32) linear_any_pair<TY_F32, MB><<<grid, 256, 0, s>>>(p_dw, p_dx);
+    else linear_any_pair<TY_BF16, MB><<<grid, 256, 0, s>>>(p_dw, p_dx);
     e = hipGetLastError();
     const unsigned n0 = finish_groups(p_dw), n1 = finish_groups(p_dx);
     if (e != hipSuccess || n0 + n1 == 0) return;

@@ -127,7 +127,7 @@ hipError_t launch_column_sums(const float* part, int G, int64_t D, float* out0, 
 // pre-activation.
 // 256 x 256 tile program (gemm_linear.hip): operands of whole 16-byte chunks.
 hipError_t launch_linear(const GemmParams& p, bool fp8, bool w_kmajor, int grid, hipStream_t s);
-// Any shape, stride and alignment, bf16 or fp32 (linear_small.hip): p.total_tiles
+// Any shape, stride and alignment, bf16, fp32 or e4m3 (W K-major; linear_small.hip): p.total_tiles
 // tiles of mb (128, 64 or 32) x 128, p.nt of them in a row, times p.splits K
 // ranges of p.ksteps_per_split steps of 128 bytes = p.units work-groups; the
 // ranges' partial sums in p.partial (16-byte aligned).  A token-major.

@@ -116,7 +116,7 @@ def test_few_rows(M, N, K, trans_w):
 
 # whole 16-byte chunks: the 256 x 256 tiles, with split K, a tail split and ragged edges
 TILES = [(65, 264, 200), (300, 264, 200), (256, 256, 64), (520, 1288, 1024), (257, 8, 4096), (1000, 512, 8), (4352, 4096, 1024),
-         (1100, 1288, 1032), (2056, 520, 2048), (257, 4104, 2048)]
+         (1100, 1288, 1032), (2056, 520, 2048), (257, 4104, 2048), (2056, 1288, 1032)]
 
 
 @pytest.mark.parametrize("M,N,K", TILES)
@@ -132,7 +132,7 @@ def test_tiles(M, N, K, trans_w):
 @pytest.mark.parametrize("act", ACTS)
 @pytest.mark.parametrize("trans_w", [False, True])
 def test_tiles_every_activation(act, trans_w):
-    for M, N, K in ((300, 520, 264), (1100, 1288, 1032)):      # small products run on other tiles
+    for M, N, K in ((300, 520, 264), (2056, 1288, 1032)):      # small products run on other tiles
         fwd_check(M, N, K, act=act, trans_w=trans_w)
         fwd_check(M, N, K, act=act, trans_w=trans_w, res=False)
 
@@ -157,8 +157,8 @@ def test_small_fp32_and_narrow(M, N, K):
 
 def test_unaligned_arrays_of_whole_chunk_shapes():
     # sizes the tiles take, addresses and strides they do not
-    fwd_check(1100, 1288, 1032, off=1)
-    fwd_check(1100, 1288, 1032, ld=4, off=4)
+    fwd_check(2056, 1288, 1032, off=1)
+    fwd_check(2056, 1288, 1032, ld=4, off=4)
     fwd_check(300, 264, 200, off=1)
     fwd_check(300, 264, 200, ld=4, off=4)
     fwd_check(300, 264, 200, ld=1)
@@ -175,7 +175,7 @@ def test_empty_contraction_and_empty_outputs():
     torch.cuda.synchronize()
 
 
-@pytest.mark.parametrize("M,N,K,dt", [(1, 264, 1000, B), (16, 100, 77, B), (300, 264, 200, B), (520, 1288, 1024, B), (1100, 1288, 1032, B), (129, 131, 67, B),
+@pytest.mark.parametrize("M,N,K,dt", [(1, 264, 1000, B), (16, 100, 77, B), (300, 264, 200, B), (520, 1288, 1024, B), (2056, 1288, 1032, B), (129, 131, 67, B),
                                       (129, 131, 67, F), (40, 264, 200, F)])
 @pytest.mark.parametrize("trans_w", [False, True])
 def test_integers_are_exact(M, N, K, dt, trans_w):
@@ -189,7 +189,8 @@ def test_integers_are_exact(M, N, K, dt, trans_w):
     assert np.array_equal(f64(Z), ref["Z"]) and np.array_equal(f64(Y), ref["Y"])
 
 
-@pytest.mark.parametrize("M,N,K", [(1, 264, 272), (300, 264, 272), (520, 1288, 2048), (4352, 4096, 2048)])
+@pytest.mark.parametrize("M,N,K", [(1, 264, 272), (300, 264, 272), (520, 1288, 2048), (4352, 4096, 2048), (1, 1280, 8192), (3, 9, 5),
+                                   (33, 70, 250), (129, 131, 67), (1100, 1288, 2064), (1100, 1283, 2061), (2056, 1288, 2064)])
 def test_fp8_operands(M, N, K):
     xq, sx = si.to_e4m3_current(si.normal_f32((M, K), 80))
     wq, sw = si.to_e4m3_current(si.normal_f32((N, K), 81, 0.02))
@@ -209,8 +210,19 @@ def test_fp8_operands(M, N, K):
     assert y_ok() and z_ok()
 
 
+@pytest.mark.parametrize("M,N,K", [(2, 70, 250), (130, 131, 300), (2056, 1288, 2064)])
+def test_fp8_integers_are_exact(M, N, K):
+    x, w, b, r = (si.small_ints(s, 85 + k) for k, s in enumerate([(M, K), (N, K), (N,), (M, N)]))
+    Y = torch.empty(M, N, dtype=F, device="cuda")
+    one = torch.ones(1, device="cuda")
+    tpm.tp_linear_fwd(si.to_e4m3_exact(x).cuda(), si.to_e4m3_exact(w).cuda(), Y, bias=dev(b, B), residual=dev(r, F), trans_w=True,
+                      x_scale=one, w_scale=one)
+    torch.cuda.synchronize()
+    assert np.array_equal(f64(Y), ops.linear_fwd(x, w.T, b, ops.ACT_NONE, r)["Y"])
+
+
 def test_residual_in_place():
-    for M, N, K in ((3, 264, 1000), (300, 264, 200), (1100, 1288, 1032), (129, 131, 67)):
+    for M, N, K in ((3, 264, 1000), (300, 264, 200), (2056, 1288, 1032), (129, 131, 67)):
         fwd_check(M, N, K, inplace=True, act=ops.ACT_RELU)
 
 
@@ -232,7 +244,7 @@ def test_chunks_in_any_order_and_gated():
     assert all(torch.equal(outs[0], y) for y in outs[1:])
 
 
-@pytest.mark.parametrize("M,N,K", [(4, 264, 1000), (300, 264, 200), (129, 131, 67), (1100, 1288, 1032)])
+@pytest.mark.parametrize("M,N,K", [(4, 264, 1000), (300, 264, 200), (129, 131, 67), (2056, 1288, 1032)])
 @pytest.mark.parametrize("trans_w", [False, True])
 def test_infinities_and_nans_stay_in_their_row_and_column(M, N, K, trans_w):
     x, w = si.normal_f32((M, K), 95), si.normal_f32((K, N), 96, 0.05)
@@ -281,6 +293,7 @@ def bwd_check(M, N, K, dt=B, act=ops.ACT_GELU_ERF, dwdt=None, dbias=True, seed=2
 
 BWD = [(1, 8, 8), (1, 1, 1), (5, 24, 16), (300, 264, 200), (301, 264, 200), (515, 771, 259), (17, 33, 129), (1000, 512, 264), (64, 1280, 1024),
        (1021, 520, 1032), (3, 600, 7), (2000, 9, 65)]
+LARGE = [(2048, 1032, 1096), (2051, 1288, 1024), (4100, 520, 1040)]     # the paired 256 x 256 tiles, whole and ragged rows
 
 
 @pytest.mark.parametrize("M,N,K", BWD)
@@ -288,6 +301,12 @@ BWD = [(1, 8, 8), (1, 1, 1), (5, 24, 16), (300, 264, 200), (301, 264, 200), (515
 def test_backward(M, N, K, dt):
     bwd_check(M, N, K, dt, ACTS[(M + N) % 5])
     bwd_check(M, N, K, dt, ACTS[(M + N + 2) % 5], dwdt=F, dbias=False)
+
+
+@pytest.mark.parametrize("M,N,K", LARGE)
+def test_backward_large(M, N, K):
+    bwd_check(M, N, K, B, ACTS[M % 5])
+    bwd_check(M, N, K, B, ops.ACT_GELU_ERF, dwdt=F, ld=8, off=8)
 
 
 @pytest.mark.parametrize("act", ACTS)

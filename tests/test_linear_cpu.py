@@ -84,8 +84,7 @@ def test_forward_refusals():
     assert _fwd(ready=FAKE) == X.EWORKSPACE
     assert _fwd(ready=FAKE, wk=FAKE, wkb=1 << 20, K=260, ldx=260) == U                  # no whole chunks: no gating
     assert _fwd(ready=FAKE, wk=FAKE, wkb=1 << 20, b=FAKE + 2) == U
-    assert _fwd(dt=X.FP8_E4M3, tw=0) == U and _fwd(dt=X.FP8_E4M3, tw=1, K=250, ldx=250, ldw=250) == U
-    assert _fwd(dt=X.FP8_E4M3, tw=1, r=FAKE + 2, ldr=256) == U
+    assert _fwd(dt=X.FP8_E4M3, tw=0) == U
     assert "tp_linear_fwd" in X.last_error()
     assert _fwd(M=0) == X.OK and _fwd(N=0, ldw=0, ldy=0) == X.OK
 
