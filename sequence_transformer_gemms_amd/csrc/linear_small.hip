@@ -61,41 +61,55 @@ __device__ __forceinline__ void finish4(const GemmParams& p, f32x4 v, const f32x
   store4(p.Y, p.y_f32, row * p.ldy + col, n, v + r);
 }
 
-// Sums of the K ranges, then the epilogue.  The partial sums are laid out by
-// tile, part[range][tile][MB][128]; only the rows inside the matrix are written
-// and read.  A work-group takes one row of a tile: 32 threads for its 128
-// columns, times eight that add every eighth range (few dependent loads: a
-// decoding step has tens of ranges) and whose sums are added in order.
+// Sums of the K ranges, in ascending order, then the epilogue.  The partial sums
+// are laid out by tile, part[range][tile][MB][128]; only the rows inside the
+// matrix are written and read; 32 threads take the 128 columns of a row.  Up to
+// eight ranges: a work-group takes eight rows.  More (a decoding step has tens):
+// it takes one row, and eight times 32 threads add every eighth range, few
+// dependent loads each, whose sums are added in order.
+constexpr int kFinishRows = 8;
 template <int MB>
-__device__ __forceinline__ void finish_row(const GemmParams& p, int u, f32x4 (&red)[8][32]) {
+__device__ __forceinline__ void finish_unit(const GemmParams& p, int u, f32x4 (&red)[8][32]) {
   const int q = threadIdx.x & 31, slice = threadIdx.x >> 5;
-  const int row = u / p.nt, strip = u - row * p.nt, tile = strip * p.mt_per_group + row / MB, col = strip * kAnyTile + 4 * q;
+  const bool many = p.splits > kFinishRows;
+  const int strip = u % p.nt, row = many ? u / p.nt : u / p.nt * kFinishRows + slice, col = strip * kAnyTile + 4 * q;
+  const int tile = strip * p.mt_per_group + row / MB;
   const f32x4* src = (const f32x4*)(p.partial + ((int64_t)tile * MB + row % MB) * kAnyTile) + q;
   const int64_t range = (int64_t)p.total_tiles * MB * kAnyTile / 4;
-  f32x4 s = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll 4
-  for (int i = slice; i < p.splits; i += 8) s += src[i * range];
-  red[slice][q] = s;
   const float scale = scale_of(p);
-  __syncthreads();
-  if (slice != 0 || col >= p.N) return;
-  const f32x4 bias = bias4(p, col), r = resid4(p, row, col);
+  f32x4 s = {0.f, 0.f, 0.f, 0.f}, bias = s, r = s;
+  if (many) {
+#pragma unroll 4
+    for (int i = slice; i < p.splits; i += 8) s += src[i * range];
+    red[slice][q] = s;
+    __syncthreads();
+    if (slice != 0 || col >= p.N) return;
+    bias = bias4(p, col);
+    r = resid4(p, row, col);
 #pragma unroll
-  for (int i = 1; i < 8; ++i) s += red[i][q];
+    for (int i = 1; i < 8; ++i) s += red[i][q];
+  } else {
+    if (row >= p.M || col >= p.N) return;
+    bias = bias4(p, col);
+    r = resid4(p, row, col);
+#pragma unroll
+    for (int i = 0; i < kFinishRows; ++i)
+      if (i < p.splits) s += src[i * range];
+  }
   s = s * scale + bias;
   with_act(p.act, [&](auto ac) { finish4<decltype(ac)::value>(p, s, r, row, col); });
 }
 template <int MB>
 __global__ void __launch_bounds__(256) finish_ranges(const GemmParams p) {
   __shared__ f32x4 red[8][32];
-  finish_row<MB>(p, blockIdx.x, red);
+  finish_unit<MB>(p, blockIdx.x, red);
 }
 // of two products: the first n0 work-groups are p0's
 template <int MB>
 __global__ void __launch_bounds__(256) finish_ranges_pair(const GemmParams p0, const GemmParams p1, int n0) {
   __shared__ f32x4 red[8][32];
-  if ((int)blockIdx.x < n0) finish_row<MB>(p0, blockIdx.x, red);
-  else finish_row<MB>(p1, (int)blockIdx.x - n0, red);
+  if ((int)blockIdx.x < n0) finish_unit<MB>(p0, blockIdx.x, red);
+  else finish_unit<MB>(p1, (int)blockIdx.x - n0, red);
 }
 
 // -------------------------------------------------------------- any shape
@@ -475,8 +489,11 @@ void with_tile(int mb, F&& f) {
   else f(std::integral_constant<int, kAnyTile>{});
 }
 
-// work-groups of the finalisation: one per row and strip of 128 columns
-unsigned finish_groups(const GemmParams& p) { return p.splits > 1 ? (unsigned)p.M * (unsigned)p.nt : 0u; }
+// work-groups of the finalisation (finish_unit)
+unsigned finish_groups(const GemmParams& p) {
+  const int rows = p.splits > kFinishRows ? p.M : (p.M + kFinishRows - 1) / kFinishRows;
+  return p.splits > 1 ? (unsigned)rows * (unsigned)p.nt : 0u;
+}
 
 }  // namespace
 
