@@ -387,9 +387,10 @@ int partial_reduce_seqshard(int T, int64_t M, int64_t D, int rank,
  * y is computed from the unrounded v.  The sum of squares is fp32: a row
  * whose squares exceed its range gives rstd = 0.  A row holding an infinity
  * or a NaN gives NaN where IEEE arithmetic does; other rows are untouched.
- * Whole 16-byte chunks (D and every leading dimension and partial_stride a
- * multiple of 8, 16-byte aligned arrays, D <= 32768) take a kernel that reads
- * each input once; anything else a two-pass kernel with the same rounding.
+ * For the 8-bit forms rstd and the products are carried past fp32, so that y
+ * is rounded to fp32 once before its quantisation.  Arrays need their
+ * elements' alignment only.  8 <= D <= 32768 takes a kernel that reads each
+ * input once; other D a kernel that reads it twice, with the same formulas.
  * No workspace.  Asynchronous on `stream`.
  */
 int tp_rmsnorm_fwd(int T, int64_t rows, int64_t D,
@@ -415,8 +416,9 @@ int tp_rmsnorm_fwd(int T, int64_t rows, int64_t D,
  * dh_dtype.  dh may be dres's buffer (same type and leading dimension), or
  * dy's with T = 1 (likewise).  dgamma, dbias: [D] fp32 or NULL: this slice's
  * sums (the ranks' slices add up).  Column sums are taken in fp32 in an order
- * that depends on rows and D alone, so results are repeatable bit for bit;
- * rows == 0 sets them to zero.
+ * that depends on rows, D, T and the types alone, so results are repeatable
+ * bit for bit; rows == 0 sets them to zero.  8 <= D <= 16384 reads each input
+ * once, other D twice.
  * workspace >= tpm_workspace_bytes(TPM_OP_RMSNORM_BWD, rows, D, 0, T, 1,
  * dy_dtype) bytes when dgamma or dbias is given; its contents need no
  * preparation.  Calls that share one must not overlap in time.
