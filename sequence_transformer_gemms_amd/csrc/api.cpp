@@ -928,10 +928,11 @@ int tp_linear_act_bwd(int64_t M, int64_t N, int64_t K,
                 dX, lddx, dtype, TPM_EPI_FWD, TPM_ACT_NONE, nullptr, 0, nullptr,
                 1, nullptr, nullptr, nullptr, 0, ctrl, part, part_bytes};
   hipError_t e = hipSuccess;
+  BandSums sums{nullptr, 0, N, nullptr};
   if (M > 0 && N > 0 && (Z || dbias)) {
     const int nb = dact_bands(M, N);
+    if (dbias) sums = BandSums{bands, nb, N, dbias};
     e = launch_dact_columns(dY, lddy, Z, ldz, dtype == TPM_F32, act, M, N, Z ? dZ : nullptr, dbias ? bands : nullptr, nb, s);
-    if (e == hipSuccess && dbias) e = launch_column_sums(bands, nb, N, dbias, nullptr, s);
   } else if (dbias && N > 0) {
     e = launch_ctrl_init((uint32_t*)dbias, (int)N, s);   // the sum over no rows
   }
@@ -939,7 +940,7 @@ int tp_linear_act_bwd(int64_t M, int64_t N, int64_t K,
   // The paired tile launch reads dW's operands MN-major, so any number of
   // rows M will do there: only the other conditions of the fast path count.
   // Up to about 8 GFLOP the any-shape kernel's smaller tiles fill the chip
-  // better (64 x 512 x 512 13 us and 32; 1024^3 28 and 46; 2048 x 1024 x 1024 42
+  // better (64 x 512 x 512 11 us and 32; 1024^3 25 and 46; 2048 x 1024 x 1024 36
   // and 50; 2048^3 79 both; 8192 x 1280 x 1024 134 and 95).
   GemmDesc f_dw = g_dw;
   f_dw.K = (M + 7) / 8 * 8;
@@ -953,7 +954,8 @@ int tp_linear_act_bwd(int64_t M, int64_t N, int64_t K,
     make_params(g_dx, SplitPlan{S[1]}, p_dx);
     const int grid = std::max(8, std::min(stream_cus(s), p_dw.units + p_dx.units));
     const int first = p_dx.ksteps_per_split > p_dw.ksteps_per_split ? 1 : 0;
-    e = launch_ctrl_init(ctrl + kCtrlQueue, 8, s);
+    if (sums.out) e = launch_column_sums(sums.bands, sums.count, N, sums.out, nullptr, s);
+    if (e == hipSuccess) e = launch_ctrl_init(ctrl + kCtrlQueue, 8, s);
     if (e == hipSuccess) e = launch_gemm_pair_bf16(p_dw, false, false, p_dx, true, true, first, ctrl + kCtrlQueue, grid, s);
     return e == hipSuccess ? TPM_OK : hip_fail(e, who);
   }
@@ -964,8 +966,7 @@ int tp_linear_act_bwd(int64_t M, int64_t N, int64_t K,
   make_params(g_dx, SplitPlan{}, p_dx);
   any_params(r[0], part, p_dw);      // (an empty product has no tiles, hence no units)
   any_params(r[1], (float*)((char*)part + range_bytes(r[0], K, N)), p_dx);
-  if (p_dw.units + p_dx.units == 0) return TPM_OK;
-  e = launch_linear_any_pair(p_dw, p_dx, r[0].mb, s);
+  e = launch_linear_any_pair(p_dw, p_dx, sums, r[0].mb, s);
   return e == hipSuccess ? TPM_OK : hip_fail(e, who);
 }
 

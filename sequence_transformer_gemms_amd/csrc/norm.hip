@@ -429,28 +429,12 @@ __global__ void __launch_bounds__(1024) norm_bwd_vec(const NormParams p, int NT)
 }
 
 // Column sums of fp32 partial rows: out0 of src [G, D], and out1 of the [G, D]
-// behind it (either may be null).  A work-group takes 64 columns (a wave's
-// lanes, 256 contiguous bytes of a partial row); its 16 waves add every 16th
-// row each, and the wave sums are added in wave order: a fixed order, and 256
-// work-groups at D = 8192 with both sums.
+// behind it (either may be null).  256 work-groups of 16 waves at D = 8192
+// with both sums.
 __global__ void __launch_bounds__(1024) column_sums(const float* part, int G, int64_t D, float* out0, float* out1) {
-  __shared__ float red[16][64];
-  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-  const int64_t c = (int64_t)blockIdx.x * 64 + lane;
+  __shared__ float red[16 * 64];
   const bool second = blockIdx.y == 1 || !out0;
-  float* out = second ? out1 : out0;
-  float s = 0.f;
-  if (c < D) {
-    const float* src = part + (second ? (int64_t)G * D : 0) + c;
-#pragma unroll 8
-    for (int g = wave; g < G; g += 16) s += src[(int64_t)g * D];
-  }
-  red[wave][lane] = s;
-  __syncthreads();
-  if (wave == 0 && c < D) {
-    for (int w = 1; w < 16; ++w) s += red[w][lane];
-    out[c] = s;
-  }
+  sum_columns<16>(part + (second ? (int64_t)G * D : 0), G, D, (int64_t)blockIdx.x * 64, red, second ? out1 : out0);
 }
 
 }  // namespace

@@ -97,4 +97,25 @@ __device__ __forceinline__ void codes8(uint8_t* p, const float (&y)[8], int shif
 }
 }  // namespace
 
+// out[c] = sum over g < G of src[g, c] for the 64 columns from c0, by a
+// work-group of WAVES waves: a wave's lanes read 256 contiguous bytes of every
+// WAVES-th row, and the wave sums are added in wave order.  red: WAVES * 64
+// floats of LDS.
+template <int WAVES>
+__device__ __forceinline__ void sum_columns(const float* src, int G, int64_t D, int64_t c0, float* red, float* out) {
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  const int64_t c = c0 + lane;
+  float s = 0.f;
+  if (c < D) {
+#pragma unroll 8
+    for (int g = wave; g < G; g += WAVES) s += src[(int64_t)g * D + c];
+  }
+  red[wave * 64 + lane] = s;
+  __syncthreads();
+  if (wave == 0 && c < D) {
+    for (int w = 1; w < WAVES; ++w) s += red[w * 64 + lane];
+    out[c] = s;
+  }
+}
+
 }  // namespace tpm

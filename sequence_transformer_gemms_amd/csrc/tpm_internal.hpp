@@ -132,8 +132,15 @@ hipError_t launch_linear(const GemmParams& p, bool fp8, bool w_kmajor, int grid,
 // ranges of p.ksteps_per_split steps of 128 bytes = p.units work-groups; the
 // ranges' partial sums in p.partial (16-byte aligned).  A token-major.
 hipError_t launch_linear_any(const GemmParams& p, int mb, bool w_kmajor, hipStream_t s);
-// dW (both operands MN-major) and dX (both K-major) in one launch
-hipError_t launch_linear_any_pair(const GemmParams& p_dw, const GemmParams& p_dx, int mb, hipStream_t s);
+// dW (both operands MN-major) and dX (both K-major) in one launch and, with
+// b.out, the sums over b.count bands of the N columns.
+struct BandSums {
+  const float* bands;
+  int count;
+  int64_t N;
+  float* out;
+};
+hipError_t launch_linear_any_pair(const GemmParams& p_dw, const GemmParams& p_dx, const BandSums& b, int mb, hipStream_t s);
 constexpr int kAnyTile = 128;
 // dZ = dY * act'(Z) [M, N] (ld N; null: not stored, Z null: dZ = dY) and its
 // column sums per band of rows, part [bands, N] (null: none).
