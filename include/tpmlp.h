@@ -278,7 +278,7 @@ int tp_linear_bwd(int64_t M, int64_t N, int64_t K,
  *   Y = act(Z) + residual
  *
  * X [M, ldx >= K], W [K, ldw >= N], or with trans_w stored [N, ldw >= K];
- * dtype (of X and W) BF16, F32 or FP8_E4M3; fp32 accumulation.  x_scale,
+ * M, N and K up to 2^27; dtype (of X and W) BF16, F32 or FP8_E4M3; fp32 accumulation.  x_scale,
  * w_scale: device fp32 dequantisation factors or NULL for 1.
  * bias [N] (bias_dtype BF16 or F32) or NULL; residual [M, ldr >= N] of
  * y_dtype or NULL; Z [M, ldz >= N] of y_dtype or NULL receives the
@@ -320,12 +320,12 @@ int tp_linear_fwd(int64_t M, int64_t N, int64_t K,
  * The residual's gradient is dY itself.  X [M, ldx >= K], W [K, ldw >= N],
  * Z and dY [M, >= N], dX [M, lddx >= K] of dtype; dW [K, lddw >= N] of
  * dw_dtype (F32 with F32 inputs).  Z is not read with TPM_ACT_NONE (may be
- * NULL).  dbias [N] fp32 or NULL.  Any sizes: M == 0 writes zeros to dW and
- * dbias, N == 0 zeros to dX (empty arrays may be NULL).  The two products run
- * as tp_linear_bwd's paired launch where N and K are multiples of 8 and the
- * arrays are 16-byte aligned with leading dimensions that are multiples of 8
- * (outputs of 4), for any M; otherwise, and for F32, on the any-shape
- * matrix-core kernel.
+ * NULL).  dbias [N] fp32 or NULL.  Sizes up to 2^27: M == 0 writes zeros to
+ * dW and dbias, N == 0 zeros to dX (empty arrays may be NULL).  The two
+ * products run as tp_linear_bwd's paired launch where N and K are multiples
+ * of 8 and the arrays are 16-byte aligned with leading dimensions that are
+ * multiples of 8 (outputs of 4), for any M; otherwise, for small products and
+ * for F32, on the any-shape matrix-core kernel.
  * Results do not depend on timing.  workspace (16-byte aligned) >=
  * tpm_workspace_bytes(TPM_OP_LINEAR_ACT_BWD, M, N, K, 1, 1, dtype), contents
  * arbitrary; calls that share one must not overlap in time.
@@ -366,7 +366,7 @@ int partial_reduce_seqshard(int T, int64_t M, int64_t D, int rank,
  *   rstd[i] = 1 / sqrt(mean(v[i, :]^2) + eps)
  *   h = v  (stored),   y[i, :] = v[i, :] * rstd[i] * gamma
  *
- * rows = the slice's tokens (M/T), any count >= 0; D >= 1, any value.
+ * rows = the slice's tokens (M/T), any count >= 0; 1 <= D <= 2^27.
  * partials: P_t starts at partials + t * partial_stride elements, leading
  *    dimension ldx >= D, x_dtype BF16 or F32.  For a [T, M, D] stack pass the
  *    address of row rank * M/T; T = 1 is a plain input.
@@ -419,8 +419,8 @@ int tp_rmsnorm_fwd(int T, int64_t rows, int64_t D,
  * that depends on rows, D, T and the types alone, so results are repeatable
  * bit for bit; rows == 0 sets them to zero.  8 <= D <= 16384 reads each input
  * once, other D twice.
- * workspace >= tpm_workspace_bytes(TPM_OP_RMSNORM_BWD, rows, D, 0, T, 1,
- * dy_dtype) bytes when dgamma or dbias is given; its contents need no
+ * workspace (16-byte aligned) >= tpm_workspace_bytes(TPM_OP_RMSNORM_BWD,
+ * rows, D, 0, T, 1, dy_dtype) bytes when dgamma or dbias is given; its contents need no
  * preparation.  Calls that share one must not overlap in time.
  */
 int tp_rmsnorm_bwd(int T, int64_t rows, int64_t D,

@@ -706,6 +706,9 @@ namespace {
 // Whether p may be passed for an array of n elements.
 bool given(const void* p, int64_t n) { return p != nullptr || n == 0; }
 bool float_dt(int dt) { return dt == TPM_F32 || dt == TPM_BF16; }
+// Longest row, and longest side of a linear layer: a launch has fewer than 2^32
+// threads (16 a column in the column sums), and tile edges are 32-bit sums.
+constexpr int64_t kMaxSide = int64_t(1) << 27;
 
 int check_norm(const char* who, int T, int64_t rows, int64_t D, int64_t stride, int64_t ldx, int x_dtype, int h_dtype,
                int gamma_dtype) {
@@ -714,7 +717,7 @@ int check_norm(const char* who, int T, int64_t rows, int64_t D, int64_t stride, 
   if (!float_dt(x_dtype) || !float_dt(h_dtype) || !float_dt(gamma_dtype))
     return fail(TPM_EINVAL, "%s: input dtypes are BF16 or F32", who);
   if (rows > 0 && D == 0) return fail(TPM_EINVAL, "%s: rows of no elements have no mean", who);
-  if (rows > INT32_MAX || D > INT32_MAX) return fail(TPM_EUNSUPPORTED, "%s: size >= 2^31", who);
+  if (rows > INT32_MAX || D > kMaxSide) return fail(TPM_EUNSUPPORTED, "%s: rows >= 2^31 or D > 2^27", who);
   if (ldx < D) return fail(TPM_EINVAL, "%s: leading dimension smaller than the row width", who);
   if (T > 1 && stride < 0) return fail(TPM_EINVAL, "%s: negative partial stride", who);
   return TPM_OK;
@@ -781,6 +784,7 @@ int tp_rmsnorm_bwd(int T, int64_t rows, int64_t D,
   const size_t need = tpm_workspace_bytes(TPM_OP_RMSNORM_BWD, rows, D, 0, T, 1, dy_dtype);
   if ((dgamma || dbias) && need > 0 && (!workspace || workspace_bytes < need))
     return fail(TPM_EWORKSPACE, "%s: workspace of %zu bytes required", who, need);
+  if ((dgamma || dbias) && !aligned16(workspace)) return fail(TPM_EINVAL, "%s: workspace not 16-byte aligned", who);
   hipStream_t s = (hipStream_t)stream;
   if (rows == 0) {   // the sum over no rows
     for (float* g : {dgamma, dbias}) {
@@ -840,6 +844,7 @@ int tp_linear_fwd(int64_t M, int64_t N, int64_t K,
   const char* who = "tp_linear_fwd";
   if (dtype != TPM_F32 && dtype != TPM_BF16 && dtype != TPM_FP8_E4M3)
     return fail(TPM_EINVAL, "%s: dtype F32, BF16 or FP8_E4M3", who);
+  if (M > kMaxSide || N > kMaxSide || K > kMaxSide) return fail(TPM_EUNSUPPORTED, "%s: size > 2^27", who);
   if (bias && !float_dt(bias_dtype)) return fail(TPM_EINVAL, "%s: bias dtype BF16 or F32", who);
   if (!float_dt(y_dtype)) return fail(TPM_EINVAL, "%s: y dtype BF16 or F32", who);
   if (residual && ldr < N) return fail(TPM_EINVAL, "%s: leading dimension smaller than the row width", who);
@@ -896,7 +901,7 @@ int tp_linear_act_bwd(int64_t M, int64_t N, int64_t K,
                       void* workspace, size_t workspace_bytes, void* stream) {
   const char* who = "tp_linear_act_bwd";
   if (M < 0 || N < 0 || K < 0) return fail(TPM_EINVAL, "%s: negative size", who);
-  if (M > INT32_MAX || N > INT32_MAX || K > INT32_MAX) return fail(TPM_EUNSUPPORTED, "%s: size >= 2^31", who);
+  if (M > kMaxSide || N > kMaxSide || K > kMaxSide) return fail(TPM_EUNSUPPORTED, "%s: size > 2^27", who);
   if (!float_dt(dtype) || !float_dt(dw_dtype)) return fail(TPM_EINVAL, "%s: dtypes BF16 or F32", who);
   if (dtype == TPM_F32 && dw_dtype != TPM_F32) return fail(TPM_EUNSUPPORTED, "%s: fp32 inputs give fp32 dW", who);
   if (act < TPM_ACT_NONE || act > TPM_ACT_SILU) return fail(TPM_EINVAL, "%s: bad activation", who);

@@ -138,3 +138,11 @@ def test_binding_refusals():
         tpm.tp_linear_act_bwd(x, w, y, torch.empty(16, 8), torch.empty(4, 8))
     with pytest.raises(ValueError, match="dbias has dtype"):
         tpm.tp_linear_act_bwd(x, w, y, torch.empty(8, 16), torch.empty(4, 8), dbias=torch.empty(16, dtype=torch.bfloat16))
+
+
+@needs_lib
+def test_size_limit():
+    from sequence_transformer_gemms_amd import _abi as X
+    big = 2**27 + 1
+    assert _fwd(M=big) == _fwd(N=big, ldw=big, ldy=big) == _fwd(K=big, ldx=big) == X.EUNSUPPORTED
+    assert _bwd(M=big) == _bwd(N=big, ldw=big, ldz=big, lddy=big, lddw=big) == _bwd(K=big, ldx=big, lddx=big) == X.EUNSUPPORTED

@@ -141,3 +141,14 @@ def test_binding_refusals():
         tpm.tp_rmsnorm_bwd(x, x, torch.ones(4, dtype=torch.bfloat16), g, torch.empty(4, 8))
     with pytest.raises(ValueError, match="dres has dtype"):
         tpm.tp_rmsnorm_bwd(x, x, torch.ones(4), g, torch.empty(4, 8), dres=torch.zeros(4, 8, dtype=torch.bfloat16))
+
+
+@needs_lib
+def test_limits_and_workspace_alignment():
+    """Rows past 2^27 elements and a backward workspace off 16 bytes are
+    refused before anything is enqueued."""
+    from sequence_transformer_gemms_amd import _abi as X
+    D = 2**27 + 1
+    assert _fwd(D=D, ldx=D, ldy=D) == X.EUNSUPPORTED
+    assert _bwd(D=D, lddy=D, ldh=D, lddh=D) == X.EUNSUPPORTED
+    assert _bwd(dg=FAKE, ws=FAKE + 4, wsb=1 << 30) == X.EINVAL and "aligned" in X.last_error()
