@@ -179,13 +179,12 @@ __global__ void __launch_bounds__(256) norm_bwd_any(const NormParams p) {
 // accesses), so rows of odd width or stride run here too: where D % 8 != 0
 // the row's last chunk is loaded from column D - 8, `shift` of its elements
 // belong to the chunk before it, are zeroed, and are not stored.
-// v = the sum of the T partials of one chunk, fp32 in ascending t, up to B
-// loads in flight after the first
+// v += the partials t .. T - 1 of one chunk at `at`, fp32 in ascending t, up to
+// B loads in flight; sum_partials: v = all of them
 template <bool F32, int B>
-__device__ __forceinline__ void sum_partials(const NormParams& p, int64_t at, float (&v)[8]) {
-  widen8<F32>(load8<F32>(p.x, at), v);
+__device__ __forceinline__ void add_partials(const NormParams& p, int64_t at, int t, float (&v)[8]) {
 #pragma unroll 1
-  for (int t = 1; t < p.T; t += B) {
+  for (; t < p.T; t += B) {
     Raw8<F32> q[B];
 #pragma unroll
     for (int k = 0; k < B; ++k)
@@ -199,6 +198,12 @@ __device__ __forceinline__ void sum_partials(const NormParams& p, int64_t at, fl
         for (int e = 0; e < 8; ++e) v[e] += w[e];
       }
   }
+}
+
+template <bool F32, int B>
+__device__ __forceinline__ void sum_partials(const NormParams& p, int64_t at, float (&v)[8]) {
+  widen8<F32>(load8<F32>(p.x, at), v);
+  add_partials<F32, B>(p, at, 1, v);
 }
 
 // Sum over the `waves` (1 .. 16) waves of a row, whose first wave in the
@@ -338,7 +343,11 @@ __global__ void __launch_bounds__(1024, 4) norm_fwd_vec(const NormParams p, int 
 // Backward.  A work-group holds blockDim / NT rows at a time and walks the
 // rows with a stride; each thread keeps the dgamma and dbias sums of its own
 // columns over all the rows it sees.  At the end the row slots' sums are
-// added in LDS and leave as one row of partial sums per work-group.
+// added in LDS and leave as one row of partial sums per work-group.  With one
+// chunk a thread, the next row's h, dres and first partials are loaded before
+// this row's sum, whose barrier they would otherwise wait behind (T = 8, rows
+// 1024, D 8192: 41 us, 44.6 without; fp32, T = 1, rows and D 8192: 209 and 232);
+// more than two partials ahead gain nothing (42).
 template <bool XF, bool HF, int V>
 __global__ void __launch_bounds__(1024) norm_bwd_vec(const NormParams p, int NT) {
   __shared__ float red[2][16];
@@ -355,6 +364,22 @@ __global__ void __launch_bounds__(1024) norm_bwd_vec(const NormParams p, int NT)
     for (int e = 0; e < 8; ++e) sg[u][e] = sb[u][e] = 0.f;
   const float inv_d = 1.0f / (float)D;
   int par = 0;
+  constexpr int AHEAD = 2;
+  Raw8<XF> nx[AHEAD];   // V == 1: the next row's
+  Raw8<HF> nh, nd;
+  float nr = 0.f;
+  auto ahead = [&](int64_t row) {
+    int shift;
+    const int c = chunk_at(0, NT, t, D, shift);
+    if (row >= p.rows || c < 0) return;
+    nh = load8<HF>(p.h, row * p.ldh + c);
+    if (p.res) nd = load8<HF>(p.res, row * p.ldr + c);
+#pragma unroll
+    for (int k = 0; k < AHEAD; ++k)
+      if (k < p.T) nx[k] = load8<XF>(p.x, row * p.ldx + c + k * p.x_stride);
+    nr = p.rstd[row];
+  };
+  if (V == 1) ahead((int64_t)blockIdx.x * slots + slot);
   for (int64_t row0 = (int64_t)blockIdx.x * slots; row0 < p.rows; row0 += (int64_t)gridDim.x * slots, par ^= 1) {
     const int64_t row = row0 + slot;
     const bool live = row < p.rows;
@@ -362,16 +387,30 @@ __global__ void __launch_bounds__(1024) norm_bwd_vec(const NormParams p, int NT)
     float dy[V][8];
     Raw8<HF> hh[V], dres[V];
     float gx = 0.f;
-    const float r = live ? p.rstd[row] : 0.f;
+    const float r = V == 1 ? nr : live ? p.rstd[row] : 0.f;
 #pragma unroll
     for (int u = 0; u < V; ++u) {
       int shift;
       const int c = chunk_at(u, NT, t, D, shift);
       if (live && c >= 0) {
         float g[8], x[8];
-        hh[u] = load8<HF>(p.h, row * p.ldh + c);
-        if (p.res) dres[u] = load8<HF>(p.res, row * p.ldr + c);
-        sum_partials<XF, XF ? 2 : V == 1 ? 7 : 4>(p, row * p.ldx + c, dy[u]);
+        if constexpr (V == 1) {
+          hh[u] = nh;
+          dres[u] = nd;
+          widen8<XF>(nx[0], dy[u]);
+#pragma unroll
+          for (int k = 1; k < AHEAD; ++k)
+            if (k < p.T) {
+              widen8<XF>(nx[k], x);
+#pragma unroll
+              for (int e = 0; e < 8; ++e) dy[u][e] += x[e];
+            }
+          add_partials<XF, XF ? 2 : 4>(p, row * p.ldx + c, AHEAD, dy[u]);
+        } else {
+          hh[u] = load8<HF>(p.h, row * p.ldh + c);
+          if (p.res) dres[u] = load8<HF>(p.res, row * p.ldr + c);
+          sum_partials<XF, XF ? 2 : 4>(p, row * p.ldx + c, dy[u]);
+        }
         param8(p.gamma, p.g_f32, c, g);
         drop(dy[u], shift);
         widen8<HF>(hh[u], x);
@@ -384,6 +423,7 @@ __global__ void __launch_bounds__(1024) norm_bwd_vec(const NormParams p, int NT)
         }
       }
     }
+    if (V == 1) ahead(row + (int64_t)gridDim.x * slots);
     const float m = row_sum(gx, wave0, waves, red[par]) * inv_d;
     if (!live) continue;
 #pragma unroll
@@ -444,7 +484,7 @@ __global__ void __launch_bounds__(1024) column_sums(const float* part, int G, in
 // on the shape and the types alone, never on the stream or the arrays.  1024
 // threads per CU either way: 512 work-groups of 512 threads where each sees
 // eight rows or more (rows 8192, D 8192: 98 us, 104 with 256 of 1024), 256 of
-// 1024 where the partial sums' own traffic counts (T = 8, rows 1024, D 8192: 45
+// 1024 where the partial sums' own traffic counts (T = 8, rows 1024, D 8192: 41
 // us and 48; rows 8192, D 16384: 201 and 210).
 static bool many_rows(int64_t rows, int64_t D) { return rows >= 4096 && D <= 8192; }
 int norm_bwd_groups(int64_t rows, int64_t D) { return (int)std::min<int64_t>(rows, many_rows(rows, D) ? 512 : 256); }
@@ -502,9 +542,9 @@ hipError_t launch_norm_bwd(const NormParams& p, hipStream_t s) {
     norm_bwd_any<<<G, 256, 0, s>>>(p);
   } else {
     // Two chunks per thread; one where that leaves the registers for all the
-    // loads of many partials, or where fp32 arrays would spill them (T = 8, rows
-    // 1024, D 8192: 45 us, 48 with two), and for few rows, which then get
-    // work-groups of their own (rows 100, D 8192: 12 us and 17).
+    // loads of many partials, or of fp32 arrays, and of the next row (T = 8, rows
+    // 1024, D 8192: 41 us, 48 with two; fp32, T = 2, rows 1001, D 4099: 27 and
+    // 37), and for few rows, which then get work-groups of their own (rows 100, D 8192: 12 us and 17).
     const bool few = p.rows <= 256;
     const int V = p.D <= 8192 && (p.x_f32 || p.h_f32 || p.T >= 4 || few) ? 1 : 2;
     const int NT = row_threads(p.D, V);
