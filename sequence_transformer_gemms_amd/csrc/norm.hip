@@ -515,21 +515,28 @@ hipError_t launch_norm_fwd(const NormParams& p, hipStream_t s) {
   }
   // Chunks per thread.  Few rows: one, the most threads on each row.  Else
   // more bytes in flight per row and more rows per CU: rows 1024, D 8192, T = 8
-  // 33 us with four, 37 with two, 43 with one; rows 8192, D 8192, T = 1 88 us
-  // with two, 96 with four, 113 with one; rows 8192, D 16384 194 us with four,
-  // 220 with two.
+  // 33 us with four, 37 with two, 43 with one; rows 8192, D 8192, T = 1 85 us
+  // with two, 94 with four, 116 with one; rows 8192, D 16384 198 us with four,
+  // 210 with two (e4m3 191 and 222).
   int V = p.rows < 512 ? 1 : (p.T >= 4 || p.D > 8192) ? 4 : 2;
   while (p.D > 8192 * V) V *= 2;
   const int NT = row_threads(p.D, V);
   const int threads = std::max(1, 256 / NT) * NT;
   const int slots = threads / NT;
-  // a persistent grid of 2048 threads per CU
-  const int grid = (int)std::min<int64_t>((p.rows + slots - 1) / slots, (1 << 19) / threads);
+  // bf16 and fp32 outputs: every row a work-group of its own, whatever number
+  // of them a CU holds (rows 8192, D 8192 85 us, 100 with a grid of 2048 threads
+  // per CU; 16384 x 6000 150 and 167; 16384 x 2560 58 and 70; 2048 x 8192 29 both).
+  // 8-bit outputs: 1024 threads per CU, which are resident together, because
+  // the amax and the encoders' code are paid per work-group (16384 x 8192 e4m3 190
+  // us, 224 with one row each; 10000 x 1300 42 and 71, 45 with 2048 threads).
+  const bool fp8 = p.y_kind == NORM_Y_E4M3 || p.y_kind == NORM_Y_MX;
+  const int64_t most = fp8 ? 256 * (1024 / threads) : (int64_t(1) << 31) / threads;
+  const int grid = (int)std::min<int64_t>((p.rows + slots - 1) / slots, most);
   with_chunks(V, [&](auto vc) {
     with_types(p, [&](auto xf, auto hf) {
       constexpr bool XF = decltype(xf)::value, HF = decltype(hf)::value;
       constexpr int V = decltype(vc)::value;
-      if (p.y_kind == NORM_Y_E4M3 || p.y_kind == NORM_Y_MX) norm_fwd_vec<XF, HF, V, true><<<grid, threads, 0, s>>>(p, NT);
+      if (fp8) norm_fwd_vec<XF, HF, V, true><<<grid, threads, 0, s>>>(p, NT);
       else norm_fwd_vec<XF, HF, V, false><<<grid, threads, 0, s>>>(p, NT);
     });
   });
@@ -544,7 +551,8 @@ hipError_t launch_norm_bwd(const NormParams& p, hipStream_t s) {
     // Two chunks per thread; one where that leaves the registers for all the
     // loads of many partials, or of fp32 arrays, and of the next row (T = 8, rows
     // 1024, D 8192: 41 us, 48 with two; fp32, T = 2, rows 1001, D 4099: 27 and
-    // 37), and for few rows, which then get work-groups of their own (rows 100, D 8192: 12 us and 17).
+    // 37), and for few rows, which then get work-groups of their own (rows 100,
+    // D 8192: 12 us and 17).
     const bool few = p.rows <= 256;
     const int V = p.D <= 8192 && (p.x_f32 || p.h_f32 || p.T >= 4 || few) ? 1 : 2;
     const int NT = row_threads(p.D, V);
