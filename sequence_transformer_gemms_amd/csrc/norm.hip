@@ -486,11 +486,32 @@ __global__ void __launch_bounds__(1024) column_sums(const float* part, int G, in
 // eight rows or more (rows 8192, D 8192: 98 us, 104 with 256 of 1024), 256 of
 // 1024 where the partial sums' own traffic counts (T = 8, rows 1024, D 8192: 41
 // us and 48; rows 8192, D 16384: 201 and 210).
-static bool many_rows(int64_t rows, int64_t D) { return rows >= 4096 && D <= 8192; }
-int norm_bwd_groups(int64_t rows, int64_t D) { return (int)std::min<int64_t>(rows, many_rows(rows, D) ? 512 : 256); }
-
 // whole waves that cover D columns at V chunks of 8 a thread
 static int row_threads(int64_t D, int V) { return (int)((D + 512 * V - 1) / (512 * V)) * 64; }
+
+// Rows of NT threads that a work-group of the backward holds, and the most
+// work-groups.  Each sums its rows' column contributions, so their number
+// fixes the order of the column sums; it depends on the shape and the types
+// alone, never on the stream or the arrays.  Up to 1024 threads per CU either
+// way: two work-groups of about 512 where each sees eight rows or more (rows
+// 8192, D 8192: 98 us, 104 with 256 of 1024; D 7000 99 and 106), one of 1024 where
+// rows of three, five or six waves would leave more of a CU idle (rows 20000, D
+// 4099 159 and 198; 16384 x 2560 80 and 84), where the partial sums' own traffic
+// counts (T = 8, rows 1024, D 8192: 41 us and 48), and for wide rows (8192 x 16384
+// 201 and 210).
+static int bwd_slots(int64_t rows, int64_t D, int NT) {
+  const int w = NT / 64;
+  const bool two = rows >= 4096 && D <= 8192 && (16 % w == 0 || w == 7);
+  return std::max(1, (two ? 8 : 16) / w);
+}
+static int bwd_groups(int64_t rows, int64_t D, int NT) {
+  const int threads = NT * bwd_slots(rows, D, NT);
+  return (int)std::min<int64_t>(rows, rows >= 4096 && D <= 8192 && threads <= 512 ? 512 : 256);
+}
+int norm_bwd_groups(int64_t rows, int64_t D) {
+  return D > kNormMaxBwd ? (int)std::min<int64_t>(rows, 256)
+                         : std::max(bwd_groups(rows, D, row_threads(D, 1)), bwd_groups(rows, D, row_threads(D, 2)));
+}
 
 template <class F>
 static void with_types(const NormParams& p, F&& f) {
@@ -556,8 +577,8 @@ hipError_t launch_norm_bwd(const NormParams& p, hipStream_t s) {
     const bool few = p.rows <= 256;
     const int V = p.D <= 8192 && (p.x_f32 || p.h_f32 || p.T >= 4 || few) ? 1 : 2;
     const int NT = row_threads(p.D, V);
-    const int slots = few ? 1 : std::max(1, (many_rows(p.rows, p.D) ? 512 : 1024) / NT);
-    G = (int)std::min<int64_t>(G, (p.rows + slots - 1) / slots);
+    const int slots = few ? 1 : bwd_slots(p.rows, p.D, NT);
+    if (!few) G = (int)std::min<int64_t>(bwd_groups(p.rows, p.D, NT), (p.rows + slots - 1) / slots);
     const int threads = slots * NT;
     with_types(p, [&](auto xf, auto hf) {
       constexpr bool XF = decltype(xf)::value, HF = decltype(hf)::value;
