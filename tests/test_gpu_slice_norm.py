@@ -347,3 +347,33 @@ def test_other_streams_and_graph_replays():
             t.zero_()
         g.replay()
         assert all(torch.equal(a, b) for a, b in zip(results(), eager))
+
+
+@pytest.mark.parametrize("rows,D,dt", [(4097, 1300, B), (4100, 2560, B), (4099, 4099, B), (4096, 5500, B), (4097, 6200, B),
+                                       (4097, 2560, F), (4097, 4099, F), (4097, 7000, F)])
+def test_backward_of_many_rows_of_every_number_of_waves(rows, D, dt):
+    bwd_check(1, rows, D, dt, dt, dt, True, 6300 + D, inplace=D == 2560 or D == 4099)
+
+
+def test_an_infinite_gamma_saturates_the_8_bit_outputs():
+    rows, D, c = 5, 256, 70
+    i = inputs(1, rows, D, 6400)
+    p = i["p"][0]
+    p[:, c] = [1.0, -1.0, 2.0 ** -20, -3.0, 0.5]
+    x, gamma = dev(p, B), dev(i["g"], B)
+    scale = torch.tensor([4.0 / 448], device="cuda")
+    out = []
+    for g in (float(gamma[c]), float("inf")):
+        gamma[c] = g
+        y, mx = torch.empty(rows, D, dtype=torch.uint8, device="cuda"), torch.empty(rows, D, dtype=torch.uint8, device="cuda")
+        amax = torch.zeros(1, device="cuda")
+        tpm.tp_rmsnorm_fwd(x, gamma, y, y_scale=scale, amax_out=amax)
+        tpm.tp_rmsnorm_fwd(x, gamma, mx, y_scales=torch.empty(tpm.mx_scales_bytes(rows, D), dtype=torch.uint8, device="cuda"))
+        torch.cuda.synchronize()
+        out.append((formats.e4m3_to_f64(y.cpu().numpy()), formats.e4m3_to_f64(mx.cpu().numpy()), float(amax)))
+    sign = np.sign(p[:, c])
+    assert np.array_equal(out[1][0][:, c], 448.0 * sign) and np.array_equal(out[1][1][:, c], 448.0 * sign)
+    assert out[1][2] == np.inf and np.isfinite(out[0][2])
+    assert np.array_equal(np.delete(out[0][0], c, 1), np.delete(out[1][0], c, 1))
+    other = np.arange(D) // 32 != c // 32                       # the other blocks of a row
+    assert np.array_equal(out[0][1][:, other], out[1][1][:, other])
